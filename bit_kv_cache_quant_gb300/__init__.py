@@ -9,14 +9,15 @@ fallback of any kind.
 
 The functions named ``kvq_*`` / ``snapkv_*`` mirror the C entry points one
 to one; :class:`KVCache` bundles a cache buffer, its handle and a decode
-workspace for convenience.
+workspace for convenience.  :class:`Rope`, :func:`rope_qk` and
+:class:`PagedKVCache` are the rotary and paged-cache calls on torch tensors.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import re
-from ctypes import POINTER, Structure, byref, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, Structure, byref, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 from typing import Optional
 
 import torch
@@ -44,7 +45,8 @@ EVICT_KEEPSET = 1
 APPEND_CALIBRATE_K = 1
 APPEND_RECOMPUTE_K = 2
 STEP_EARLY_READ = 1
-DEV_OK, DEV_OVERFLOW, DEV_BAD_KEEPSET, DEV_TIMEOUT = 0, 1, 2, 3
+DEV_OK, DEV_OVERFLOW, DEV_BAD_KEEPSET, DEV_TIMEOUT, DEV_BAD_PAGE = 0, 1, 2, 3, 4
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4, "factors": 5}
 
 
 class kvq_config(Structure):
@@ -70,6 +72,40 @@ class kvq_stats(Structure):
     _fields_ = [("pos", c_int64), ("stored", c_int32), ("capacity", c_int32), ("device_status", c_int32),
                 ("k_calibrated", c_int32), ("cache_bytes", c_size_t), ("live_bytes", c_size_t),
                 ("tail", c_int32)]
+
+
+class kvq_rope_config(Structure):
+    _fields_ = [("rot_dim", c_int32), ("scaling", c_int32), ("base", c_double), ("factor", c_double),
+                ("original_max_position", c_double), ("beta_fast", c_double), ("beta_slow", c_double),
+                ("low_freq_factor", c_double), ("high_freq_factor", c_double), ("factors", POINTER(c_double)),
+                ("attn_factor", c_double)]
+
+
+class kvq_rope(Structure):
+    _fields_ = [("freqs", c_void_p), ("rot_dim", c_int32), ("interleaved", c_int32), ("attn_factor", c_float)]
+
+
+class kvq_rows(Structure):
+    _fields_ = [("in_", c_void_p), ("out", c_void_p), ("in_tok_stride", c_int64), ("in_head_stride", c_int64),
+                ("out_tok_stride", c_int64), ("out_head_stride", c_int64), ("heads", c_int32),
+                ("norm_weight", c_void_p)]
+
+
+class kvq_paged_config(Structure):
+    _fields_ = [("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32), ("n_pages", c_int32),
+                ("k_format", c_int32), ("k_bits", c_int32), ("k_group", c_int32),
+                ("v_format", c_int32), ("v_bits", c_int32), ("v_group", c_int32)]
+
+
+class kvq_paged_layout(Structure):
+    _fields_ = [("total_bytes", c_size_t), ("k_row_bytes", c_int32), ("v_row_bytes", c_int32),
+                ("k_n_groups", c_int32), ("v_n_groups", c_int32), ("state", c_size_t), ("k_codes", c_size_t),
+                ("k_meta", c_size_t), ("v_codes", c_size_t), ("v_meta", c_size_t)]
+
+
+class kvq_paged_batch(Structure):
+    _fields_ = [("n_seqs", c_int32), ("max_pages", c_int32), ("page_table", c_void_p), ("seq_lens", c_void_p),
+                ("max_prefix_pages", c_int32), ("prefix_pages", c_void_p), ("prefix_len", c_void_p)]
 
 
 def _proto(name, res, *args):
@@ -101,6 +137,19 @@ _proto("snapkv_pool", c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_
 _proto("snapkv_select", c_int32, c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p)
 _proto("snapkv_topk", c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p)
+_proto("kvq_rope_table", c_int32, POINTER(kvq_rope_config), POINTER(c_uint64), POINTER(c_float))
+_proto("kvq_rope_qk", c_int32, POINTER(kvq_rows), POINTER(kvq_rows), c_int32, c_int32, c_int32, c_void_p,
+       POINTER(kvq_rope), c_float, c_void_p)
+_proto("kvq_paged_layout_query", c_int32, POINTER(kvq_paged_config), POINTER(kvq_paged_layout))
+_proto("kvq_paged_init", c_int32, POINTER(kvq_paged_config), c_void_p, c_size_t, c_void_p, POINTER(c_void_p))
+_proto("kvq_paged_release", None, c_void_p)
+_proto("kvq_paged_append", c_int32, c_void_p, POINTER(kvq_paged_batch), c_int32, c_void_p, POINTER(kvq_rows),
+       POINTER(kvq_rows), POINTER(kvq_rows), c_int32, POINTER(kvq_rope), c_void_p, c_float, c_void_p)
+_proto("kvq_paged_workspace_bytes", c_size_t, c_void_p, c_int32, c_int32, c_int32)
+_proto("kvq_paged_decode_attn", c_int32, c_void_p, POINTER(kvq_paged_batch), c_void_p, c_void_p, c_int32, c_int32,
+       c_float, c_void_p, c_size_t, c_void_p)
+_proto("kvq_paged_status", c_int32, c_void_p, POINTER(c_int32))
+_proto("kvq_paged_clear_status", c_int32, c_void_p, c_void_p)
 _proto("kvq_stats_read", c_int32, c_void_p, POINTER(kvq_stats))
 _proto("kvq_clear_status", c_int32, c_void_p, c_void_p)
 _proto("kvq_last_launch_count", c_int32)
@@ -443,3 +492,274 @@ def snapkv(k: torch.Tensor, obs_window: int, budget: int, n_sink: int, want_scor
     idx = torch.empty((B, H, min(budget, S)), dtype=torch.int32, device=k.device)
     snapkv_select(k, S, B, H, S, D, obs_window, budget, n_sink, scores, idx, ws, stream)
     return scores, idx
+
+
+# ---------------------------------------------------- positions, paged cache --
+
+def kvq_paged_layout_query(cfg: kvq_paged_config) -> kvq_paged_layout:
+    lay = kvq_paged_layout()
+    _check(lib.kvq_paged_layout_query(byref(cfg), byref(lay)))
+    return lay
+
+
+def kvq_rope_table(cfg: kvq_rope_config):
+    """(table of rot_dim / 2 unsigned 64-bit turn fractions, magnitude of the sines and cosines)."""
+    freqs = (c_uint64 * max(1, cfg.rot_dim // 2))()
+    mag = c_float()
+    _check(lib.kvq_rope_table(byref(cfg), freqs, byref(mag)))
+    return list(freqs), mag.value
+
+
+def _same_device(*ts) -> torch.device:
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device per call")
+    return dev
+
+
+def _on(dev: torch.device, stream, fn):
+    """fn(raw stream) with `dev` current; `stream` as in the other calls (None: the device's current one)."""
+    if dev.index == torch.cuda.current_device():
+        return fn(torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
+    with torch.cuda.device(dev):
+        return fn(_stream(stream))
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output allocated on the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+class Rope:
+    """A rotation's frequency table on the device (kvq_rope_table): the first rot_dim channels of each head
+    turn, in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.  scaling: "none", "linear" (factor),
+    "ntk" (factor), "yarn" (factor, original_max_position, beta_fast, beta_slow), "llama3" (factor,
+    original_max_position, low_freq_factor, high_freq_factor) or "factors" (factors, one per pair)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_max_position: float = 0.0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                 factors=None, attn_factor: float = 0.0, device="cuda"):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        arr = None
+        if factors is not None:
+            factors = [float(f) for f in factors]
+            if len(factors) != rot_dim // 2:
+                raise ValueError("factors needs one value per pair")
+            arr = (c_double * len(factors))(*factors)
+        cfg = kvq_rope_config(rot_dim, ROPE_SCALINGS[scaling], base, factor, original_max_position, beta_fast,
+                              beta_slow, low_freq_factor, high_freq_factor, arr, attn_factor)
+        table, self.attn_factor = kvq_rope_table(cfg)
+        self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
+        signed = [f - (1 << 64) if f >= 1 << 63 else f for f in table]
+        self.freqs = torch.tensor(signed, dtype=torch.int64, device=device)   # the 64 bits of each entry
+        if self.freqs.is_cuda:
+            torch.cuda.current_stream(self.freqs.device).synchronize()   # usable on every stream from here on
+        self.c = kvq_rope(self.freqs.data_ptr(), rot_dim, int(self.interleaved), self.attn_factor)
+
+
+def _rows(name, x: torch.Tensor, out: Optional[torch.Tensor], weight: Optional[torch.Tensor], tokens: int,
+          head_dim: int, dtype) -> kvq_rows:
+    s = x.shape
+    if len(s) != 3 or s[0] != tokens or s[2] != head_dim or x.dtype is not dtype:
+        raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}] {dtype}, got {tuple(s)} {x.dtype}")
+    st = x.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    ost, optr, w = (0, 0), None, None
+    if out is not None:
+        if out.shape != s or out.dtype is not dtype or out.stride(2) != 1:
+            raise ValueError(f"{name}_out must have {name}'s shape and dtype, its channels contiguous")
+        ost, optr = out.stride(), out.data_ptr()
+        if (ost[0] == 0 and s[0] > 1) or (ost[1] == 0 and s[1] > 1):
+            raise ValueError(f"{name}_out must not be an expanded tensor")
+    if weight is not None:
+        if weight.shape != (head_dim,) or weight.dtype is not dtype or not weight.is_contiguous():
+            raise ValueError(f"{name}_norm must be a contiguous [{head_dim}] tensor of {name}'s dtype")
+        w = weight.data_ptr()
+    return kvq_rows(x.data_ptr(), optr, st[0], st[1], ost[0], ost[1], s[1], w)
+
+
+def _int32(name, t: Optional[torch.Tensor], shape) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+            rope: Optional[Rope], q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+            q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+            stream=None):
+    """(q_out, k_out): q and k [T, heads, D] normed (RMS over each head, times q_norm / k_norm [D], where
+    given), then rotated by positions int32 [T] (rope None: norm only).  Strided q and k, and outputs that
+    are the inputs themselves, are fine; either of q and k may be None."""
+    x = q if q is not None else k
+    if x is None or x.dim() != 3 or x.dtype not in DTYPES:
+        raise ValueError("q and k must be [T, heads, D] fp32 / bf16 / fp16 tensors")
+    dev = _same_device(q, k, positions, q_out, k_out, q_norm, k_norm, rope.freqs if rope is not None else None)
+    tokens, head_dim = x.shape[0], x.shape[2]
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, q.dtype, dev, stream)
+    if k is not None and k_out is None:
+        k_out = _empty(k.shape, k.dtype, dev, stream)
+    rq = byref(_rows("q", q, q_out, q_norm, tokens, head_dim, x.dtype)) if q is not None else None
+    rk = byref(_rows("k", k, k_out, k_norm, tokens, head_dim, x.dtype)) if k is not None else None
+    pos = _int32("positions", positions, (tokens,))
+    rp = byref(rope.c) if rope is not None else None
+    _check(_on(dev, stream, lambda st: lib.kvq_rope_qk(rq, rk, tokens, head_dim, DTYPES[x.dtype], pos, rp, eps, st)))
+    return q_out, k_out
+
+
+class PagedKVCache:
+    """One layer's pool of pages and its handle.  Page tables, lengths and the batch's shared prefix are the
+    caller's int32 device tensors, common to the pools of all layers, and are read by the kernels: a captured
+    graph follows what they hold at replay.
+
+    page_table [B, max_pages], seq_lens [B]: token j of sequence b is row j % page_size of page
+    page_table[b, j // page_size].  prefix_pages [n], prefix_len [1]: tokens in front of every sequence.
+
+    A call on a stream other than the tensors' own, or a graph, needs its own `workspace` (workspace_bytes)
+    when it may run beside another decode_attn of this pool; without one, the pool's own is used."""
+
+    def __init__(self, n_kv_heads, head_dim, page_size, n_pages, k_format="fp16", k_bits=16, k_group=0,
+                 v_format="fp16", v_bits=16, v_group=0, buf: Optional[torch.Tensor] = None, device="cuda",
+                 stream=None):
+        self.cfg = kvq_paged_config(n_kv_heads, head_dim, page_size, n_pages, FORMATS[k_format], k_bits, k_group,
+                                    FORMATS[v_format], v_bits, v_group)
+        self.layout = kvq_paged_layout_query(self.cfg)
+        if buf is None:
+            buf = torch.zeros(self.layout.total_bytes, dtype=torch.uint8, device=device)
+        if not buf.is_cuda or buf.dtype is not torch.uint8 or not buf.is_contiguous():
+            raise ValueError("buf must be a contiguous uint8 CUDA tensor")
+        self.buf = buf
+        h = c_void_p()
+        _check(_on(buf.device, stream, lambda st: lib.kvq_paged_init(byref(self.cfg), buf.data_ptr(), buf.numel(), st,
+                                                                     byref(h))))
+        self.handle = h
+        self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
+        self._ws: Optional[torch.Tensor] = None
+        self._old_ws = []
+        self._need = {}
+        self.launches = 0
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h:
+            lib.kvq_paged_release(h)
+            self.handle = None
+
+    def _batch(self, page_table, seq_lens, prefix_pages, prefix_len) -> kvq_paged_batch:
+        if page_table.dim() != 2 or page_table.shape[0] != seq_lens.shape[0]:
+            raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+        B, cols = page_table.shape
+        npre = 0 if prefix_pages is None else prefix_pages.numel()
+        if npre and prefix_len is None:
+            raise ValueError("prefix_pages needs prefix_len")
+        return kvq_paged_batch(B, cols, _int32("page_table", page_table, (B, cols)),
+                               _int32("seq_lens", seq_lens, (B,)), npre, _int32("prefix_pages", prefix_pages, (npre,)),
+                               _int32("prefix_len", prefix_len, (1,)))
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+               cu_tokens: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+               rope: Optional[Rope] = None, prefix_len: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+               k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+               q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               stream=None) -> Optional[torch.Tensor]:
+        """Stores the step's new tokens k, v [T, Hkv, D] (k normed and rotated on the way) and returns q [T, Hq, D]
+        normed and rotated.  seq_lens counts the new tokens; cu_tokens int32 [B + 1] gives each sequence's run of
+        tokens (None: one each).  k_out, v_out: where to leave the values the stored rows stand for."""
+        if k.dim() != 3 or k.dtype not in DTYPES:
+            raise ValueError("k and v must be [T, Hkv, D] fp32 / bf16 / fp16 tensors")
+        dev = _same_device(self.buf, k, v, page_table, seq_lens, cu_tokens, q, prefix_len, positions, q_out, k_out,
+                           v_out, q_norm, k_norm, rope.freqs if rope is not None else None)
+        tokens, dt = k.shape[0], k.dtype
+        batch = self._batch(page_table, seq_lens, None, prefix_len)
+        if q is not None and q_out is None:
+            q_out = _empty(q.shape, q.dtype, dev, stream)
+        rq = byref(_rows("q", q, q_out, q_norm, tokens, self.head_dim, dt)) if q is not None else None
+        rk = _rows("k", k, k_out, k_norm, tokens, self.head_dim, dt)
+        rv = _rows("v", v, v_out, None, tokens, self.head_dim, dt)
+        cu = _int32("cu_tokens", cu_tokens, (batch.n_seqs + 1,))
+        pos = _int32("positions", positions, (tokens,))
+        rp = byref(rope.c) if rope is not None else None
+        _check(_on(dev, stream, lambda st: lib.kvq_paged_append(self.handle, byref(batch), tokens, cu, rq, byref(rk),
+                                                                byref(rv), DTYPES[dt], rp, pos, eps, st)))
+        self.launches += kvq_last_launch_count()
+        return q_out
+
+    def workspace_bytes(self, n_seqs: int, n_q_heads: int, max_prefix_pages: int = 0) -> int:
+        return lib.kvq_paged_workspace_bytes(self.handle, n_seqs, n_q_heads, max_prefix_pages)
+
+    def _workspace(self, n_seqs, n_q_heads, npre, stream) -> torch.Tensor:
+        key = (n_seqs, n_q_heads, npre)
+        need = self._need.get(key)
+        if need is None:
+            need = self._need[key] = max(16, self.workspace_bytes(*key))
+        if self._ws is None or self._ws.numel() < need:
+            if self._ws is not None:
+                self._old_ws.append(self._ws)   # captured graphs may still use it
+            self._ws = _empty((need,), torch.uint8, self.buf.device, stream)
+        return self._ws
+
+    def decode_attn(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                    prefix_pages: Optional[torch.Tensor] = None, prefix_len: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, softmax_scale: float = 0.0,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of q [B, Hq, D] (bf16 / fp16) over the prefix and each sequence's own tokens."""
+        s = q.shape
+        if len(s) != 3 or s[2] != self.head_dim or q.dtype not in DTYPES or not q.is_contiguous():
+            raise ValueError(f"q must be a contiguous [B, Hq, {self.head_dim}] tensor, got {tuple(s)} {q.dtype}")
+        dev = _same_device(self.buf, q, page_table, seq_lens, prefix_pages, prefix_len, out, workspace)
+        batch = self._batch(page_table, seq_lens, prefix_pages, prefix_len)
+        if s[0] != batch.n_seqs:
+            raise ValueError("q and page_table must have one row per sequence")
+        if out is None:
+            out = _empty(s, q.dtype, dev, stream)
+        elif out.shape != s or out.dtype is not q.dtype or not out.is_contiguous():
+            raise ValueError("out must have q's shape and dtype")
+        ws = workspace if workspace is not None else self._workspace(s[0], s[1], batch.max_prefix_pages, stream)
+        _check(_on(dev, stream, lambda st: lib.kvq_paged_decode_attn(
+            self.handle, byref(batch), q.data_ptr(), out.data_ptr(), s[1], DTYPES[q.dtype], softmax_scale,
+            ws.data_ptr(), ws.numel() * ws.element_size(), st)))
+        self.launches += kvq_last_launch_count()
+        return out
+
+    def status(self) -> int:
+        """The pool's status word (DEV_*); synchronises."""
+        st = c_int32()
+        _check(_on(self.buf.device, None, lambda _: lib.kvq_paged_status(self.handle, byref(st))))
+        return st.value
+
+    def clear_status(self, stream=None) -> None:
+        _check(_on(self.buf.device, stream, lambda st: lib.kvq_paged_clear_status(self.handle, st)))
+
+    def plane(self, name: str) -> torch.Tensor:
+        """A view of plane k_codes, v_codes, k_meta or v_meta of the pool: codes fp16 [n_pages, Hkv, page_size, D]
+        or uint8 [n_pages, Hkv, page_size, row_bytes]; metadata fp16 [n_pages, Hkv, page_size, groups, 2]."""
+        side, what = name.split("_")
+        rows = (self.n_pages, self.n_kv_heads, self.page_size)
+        count = self.n_pages * self.n_kv_heads * self.page_size
+        off = getattr(self.layout, name)
+        if what == "codes":
+            rb = getattr(self.layout, f"{side}_row_bytes")
+            x = self.buf[off:off + count * rb].view(*rows, rb)
+            return x.view(torch.float16) if self.cfg.k_format == FORMATS["fp16"] else x
+        ng = getattr(self.layout, f"{side}_n_groups")
+        return self.buf[off:off + count * ng * 4].view(torch.float16).view(*rows, ng, 2)

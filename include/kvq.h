@@ -129,6 +129,8 @@ typedef enum kvq_evict_mode {
 #define KVQ_DEV_BAD_KEEPSET 2      /* keep-set not strictly ascending or beyond stored rows */
 #define KVQ_DEV_TIMEOUT 3          /* a bounded wait inside a kernel ran out; outputs of that call
                                       are unspecified */
+#define KVQ_DEV_BAD_PAGE 4         /* a paged call met a page id outside the pool, or a length its
+                                      page table does not cover; those rows were left out */
 
 typedef struct kvq_config {
   int32_t batch;        /* B >= 1 */
@@ -404,6 +406,157 @@ kvq_status snapkv_pool(const float* scores, float* pooled, int32_t batch, int32_
    [B, Hkv, S] (device), with the same rule.  Needs no workspace. */
 kvq_status snapkv_topk(const float* scores, int32_t batch, int32_t n_kv_heads, int32_t S, int32_t budget,
                        int32_t n_sink, int32_t* idx_out, cudaStream_t stream);
+
+/* --------------------------------------------------------------- positions --
+   Rotary positions of queries and keys, alone or after a per-head norm, and the
+   frequency table they share with kvq_paged_append.  The StreamingLLM + KIVI
+   page keeps keys at their absolute position ("RoPE caveat") and leaves the
+   rotation to the model; these calls are that step on the GPU.  */
+
+typedef enum kvq_rope_scaling {
+  KVQ_ROPE_NONE = 0,      /* f_i = base^(-2i / rot_dim) radians per position                     */
+  KVQ_ROPE_LINEAR = 1,    /* f_i / factor                                                        */
+  KVQ_ROPE_NTK = 2,       /* base * factor^(rot_dim / (rot_dim - 2)) in place of base            */
+  KVQ_ROPE_YARN = 3,      /* f_i / factor for pairs that turn fewer than beta_slow times within
+                             original_max_position, f_i for over beta_fast, a ramp in between;
+                             sines and cosines times 0.1 ln(factor) + 1                          */
+  KVQ_ROPE_LLAMA3 = 4,    /* the same by turns low_freq_factor / high_freq_factor, no magnitude  */
+  KVQ_ROPE_FACTORS = 5    /* f_i / factors[i] (a factor for each pair)                           */
+} kvq_rope_scaling;
+
+typedef struct kvq_rope_config {
+  int32_t rot_dim;        /* rotated channels at the front of each head: even, 2 .. head_dim      */
+  int32_t scaling;        /* kvq_rope_scaling */
+  double base;            /* > 1 */
+  double factor;          /* LINEAR, NTK, YARN, LLAMA3: >= 1 */
+  double original_max_position;                /* YARN, LLAMA3: > 0 */
+  double beta_fast, beta_slow;                 /* YARN: beta_fast > beta_slow > 0 */
+  double low_freq_factor, high_freq_factor;    /* LLAMA3: high > low > 0 */
+  const double* factors;  /* FACTORS: host, rot_dim / 2 positive values */
+  double attn_factor;     /* > 0: the magnitude of sines and cosines; 0: what the scaling says */
+} kvq_rope_config;
+
+/* Fills freqs (host, rot_dim / 2 entries) and *attn_factor; no device work.  freqs[i]
+   is f_i in whole turns times 2^64, so that the 64-bit product with an integer
+   position, which wraps, is the angle modulo one turn: exact to 2^-54 of a turn
+   and position at any distance, where a 32-bit angle loses its fraction. */
+kvq_status kvq_rope_table(const kvq_rope_config* cfg, uint64_t* freqs, float* attn_factor);
+
+typedef struct kvq_rope {
+  const uint64_t* freqs;  /* device, rot_dim / 2 entries of kvq_rope_table */
+  int32_t rot_dim;
+  int32_t interleaved;    /* 0: channel i pairs with i + rot_dim / 2; 1: 2i with 2i + 1 */
+  float attn_factor;
+} kvq_rope;
+
+/* Rows of one tensor of a call over n_tokens tokens: element (token, head, channel) at
+   token * tok_stride + head * head_stride + channel (strides in elements, so a slice of
+   a fused projection needs no copy).  Every tensor of a call has the call's dtype. */
+typedef struct kvq_rows {
+  const void* in;             /* device */
+  void* out;                  /* device; may be `in` itself with equal strides */
+  int64_t in_tok_stride, in_head_stride;
+  int64_t out_tok_stride, out_head_stride;
+  int32_t heads;              /* 0: this tensor is absent */
+  const void* norm_weight;    /* device [head_dim], or NULL for no norm */
+} kvq_rows;
+
+/* q.out, k.out = rotate(norm(in)), one launch for both (either may be absent):
+   norm(x) = x * rsqrt(mean(x^2) + eps) * weight over the head's channels, when a weight
+   is given; rotate turns pair (a, b) of the token's position p by the angle p * f_i to
+   attn_factor * (a cos - b sin, b cos + a sin) and passes channels from rot_dim on.  All of
+   it in fp32, rounded once.  rope NULL: norm only.  positions: device int32 [n_tokens], any
+   sign (a rotation by -p undoes one by p when attn_factor is 1).  head_dim 32, 64, 128 or
+   256.  n_tokens 0 enqueues nothing. */
+kvq_status kvq_rope_qk(const kvq_rows* q, const kvq_rows* k, int32_t n_tokens, int32_t head_dim, int32_t dtype,
+                       const int32_t* positions, const kvq_rope* rope, float eps, cudaStream_t stream);
+
+/* ------------------------------------------------------------- paged cache --
+   A pool of pages of page_size rows that the sequences of a batch share through page
+   tables, in the cache's storage formats, and decode attention over a prefix common to the
+   whole batch followed by each sequence's own pages. */
+
+typedef struct kvq_paged_config {
+  int32_t n_kv_heads;     /* >= 1 */
+  int32_t head_dim;       /* 64 or 128 */
+  int32_t page_size;      /* rows of a page: 16, 32, 64 or 128 */
+  int32_t n_pages;        /* n_kv_heads * page_size * n_pages below 2^31 - 128 */
+  int32_t k_format, k_bits, k_group;   /* FP16 or AFFINE_TOKEN, as kvq_config */
+  int32_t v_format, v_bits, v_group;   /* the same format and bits as K; any legal group */
+} kvq_paged_config;
+
+/* Byte offsets of the planes inside the pool's buffer, multiples of 256 (0 = absent):
+     state               device status word (256 bytes)
+     {k,v}_codes         uint8 [n_pages][Hkv][page_size][row_bytes], rows coded as in kvq_cache_layout
+     {k,v}_meta          fp16  [n_pages][Hkv][page_size][n_groups][2]: (scale, zero) of each group */
+typedef struct kvq_paged_layout {
+  size_t total_bytes;
+  int32_t k_row_bytes, v_row_bytes;
+  int32_t k_n_groups, v_n_groups;
+  size_t state, k_codes, k_meta, v_codes, v_meta;
+} kvq_paged_layout;
+
+typedef struct kvq_paged_s* kvq_paged;
+
+kvq_status kvq_paged_layout_query(const kvq_paged_config* cfg, kvq_paged_layout* out);
+
+/* A pool over the caller's device buffer (>= total_bytes, 256-byte aligned): clears the
+   status word on `stream`, leaves the pages as they are.  The handle holds no counters:
+   page tables and lengths are the caller's, and shared by the pools of all layers. */
+kvq_status kvq_paged_init(const kvq_paged_config* cfg, void* dev_mem, size_t bytes, cudaStream_t stream,
+                          kvq_paged* out);
+void kvq_paged_release(kvq_paged pool);
+
+/* The sequences of a call (all arrays device int32, read by the kernels, so a captured graph
+   follows their contents).  Sequence b holds seq_lens[b] own tokens, token j in row
+   j % page_size of page page_table[b][j / page_size]; entries past its length are not read.
+   In front of them come the prefix_len[0] tokens of prefix_pages, one prefix for the whole
+   batch (prefix_len NULL: none).  Own token j has position prefix_len + j. */
+typedef struct kvq_paged_batch {
+  int32_t n_seqs;             /* 1 .. 4096 */
+  int32_t max_pages;          /* columns of page_table */
+  const int32_t* page_table;  /* [n_seqs][max_pages] */
+  const int32_t* seq_lens;    /* [n_seqs] */
+  int32_t max_prefix_pages;   /* entries of prefix_pages */
+  const int32_t* prefix_pages;
+  const int32_t* prefix_len;  /* [1] */
+} kvq_paged_batch;
+
+/* Appends the new tokens of a step, with the rotation (and norms) of kvq_rope_qk on the way:
+   k is normed, rotated and stored, v stored as it is, q (optional) normed and rotated to
+   q.out, in one launch.  seq_lens counts the new tokens: sequence b's are its last ones.
+   cu_tokens: device int32 [n_seqs + 1], tokens cu_tokens[b] .. cu_tokens[b + 1] - 1 of q, k
+   and v belong to sequence b; NULL: one token each, n_tokens == n_seqs.  Tokens outside every
+   sequence, and those that seq_lens leaves no place for (a padded row of length 0), write
+   nothing.  k.out, v.out (optional, NULL for none): the values the stored rows stand for,
+   rounded to `dtype`, so that a prompt can attend over what decode will read.  Rows are coded
+   from the fp32 values by kvq_append's rules.  rope NULL: keys are stored unrotated;
+   positions (optional): device int32 [n_tokens] in place of prefix_len + j.  v.norm_weight
+   must be NULL.  prefix_pages is not read: append a prefix as a sequence of its own.  Bad
+   pages set KVQ_DEV_BAD_PAGE and store nothing. */
+kvq_status kvq_paged_append(kvq_paged pool, const kvq_paged_batch* batch, int32_t n_tokens, const int32_t* cu_tokens,
+                            const kvq_rows* q, const kvq_rows* k, const kvq_rows* v, int32_t dtype,
+                            const kvq_rope* rope, const int32_t* positions, float eps, cudaStream_t stream);
+
+/* Workspace bytes kvq_paged_decode_attn needs for batches of up to n_seqs sequences and
+   max_prefix_pages prefix pages. */
+size_t kvq_paged_workspace_bytes(kvq_paged pool, int32_t n_seqs, int32_t n_q_heads, int32_t max_prefix_pages);
+
+/* Decode attention, one query token for each sequence, over the prefix and the sequence's own
+   tokens: out[b,h] = softmax(q . k_hat^T * softmax_scale) v_hat, as kvq_decode_attn.  q, out:
+   device [n_seqs, Hq, D] of io_dtype (bf16 / fp16), 16-byte aligned; Hq / Hkv from 1 to 8.
+   A sequence with neither prefix nor own tokens gets zeros.  workspace: 16-byte aligned device
+   memory of this call alone until it has run; calls on several streams, or graphs that may
+   replay together, each need their own.  Needs no initial contents and keeps none. */
+kvq_status kvq_paged_decode_attn(kvq_paged pool, const kvq_paged_batch* batch, const void* q, void* out,
+                                 int32_t n_q_heads, int32_t io_dtype, float softmax_scale, void* workspace,
+                                 size_t ws_bytes, cudaStream_t stream);
+
+/* Synchronises the device and returns the pool's status word (KVQ_DEV_*) in *status. */
+kvq_status kvq_paged_status(kvq_paged pool, int32_t* status);
+
+/* Clears the pool's status word (stream-ordered). */
+kvq_status kvq_paged_clear_status(kvq_paged pool, cudaStream_t stream);
 
 /* Synchronises the device, copies `cache`'s counters to the host and fills `*out`. */
 kvq_status kvq_stats_read(kvq_cache cache, kvq_stats* out);
