@@ -1,6 +1,12 @@
-// Rotary positions, per-head norms and the paged append: one warp takes one
-// token and a run of its head rows, lane l the channels [l E, l E + E) with
-// E = head_dim / 32.
+// Rotary positions, per-head norms and the paged append.
+//
+// Two kernels.  token_rows_kernel takes any layout: one warp per token and
+// run of head rows, lane l the channels [l E, l E + E) with E = head_dim / 32,
+// partners of a pair found by shuffles.  token_chunks_kernel takes rows whose
+// starts are 16-byte aligned: a lane holds two runs of eight channels, c and
+// c + D / 2 on, so that both channels of a pair sit in one lane (half layout
+// over the whole head, or interleaved) and D / 16 lanes make a row: about a
+// sixth of the instructions per element.
 //
 // A row is loaded once, normed and rotated in registers and leaves either as
 // a row of the output tensor or as codes in its page (or both), so that
@@ -294,8 +300,306 @@ __global__ void __launch_bounds__(32 * kRowWarps) token_rows_kernel(const __grid
   }
 }
 
-template <int E, typename T>
-cudaError_t launch_typed(const TokenArgs& a, bool paged, unsigned grid, cudaStream_t st) {
+// ------------------------------------------------- sixteen channels a lane --
+
+// Eight consecutive elements, 16-byte aligned.
+template <typename T> struct Eight {
+  static constexpr int N = 8 * (int)sizeof(T) / 16;
+  uint4 v[N];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+  }
+};
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, const __nv_bfloat16*) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, const __half*) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __half*) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Eight<T>& e, float* x) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(e.v[i].x);
+      x[4 * i + 1] = __uint_as_float(e.v[i].y);
+      x[4 * i + 2] = __uint_as_float(e.v[i].z);
+      x[4 * i + 3] = __uint_as_float(e.v[i].w);
+    }
+  } else {
+    const T* t = nullptr;
+    unpack2(e.v[0].x, x[0], x[1], t);
+    unpack2(e.v[0].y, x[2], x[3], t);
+    unpack2(e.v[0].z, x[4], x[5], t);
+    unpack2(e.v[0].w, x[6], x[7], t);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Eight<T> pack8(const float* x) {
+  Eight<T> e;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      e.v[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
+                          __float_as_uint(x[4 * i + 3]));
+  } else {
+    const T* t = nullptr;
+    e.v[0] = make_uint4(pack2(x[0], x[1], t), pack2(x[2], x[3], t), pack2(x[4], x[5], t), pack2(x[6], x[7], t));
+  }
+  return e;
+}
+
+// How the pairs of a lane's channels x[0..8) = c .. c + 7 and x[8..16) = D / 2 + c .. lie.
+enum ChunkPairing : int {
+  kStraight = 0,      // no rotation
+  kHalves = 1,        // half layout over the whole head: x[i] with x[8 + i]
+  kNeighbours = 2,    // interleaved: x[2i] with x[2i + 1]
+  kQuarter = 3,       // half layout over the first D / 2 channels: x[i], i < 8, with another lane's
+};
+
+// Codes eight channels with the group's quotient (affine_code_inv), stores them
+// and leaves the values they stand for.
+__device__ __forceinline__ void code_eight(uint8_t* dst, int bits, float* x, float sc, float inv, float mn, float s,
+                                           float z, bool live) {
+  const float levels = bits == 8 ? 255.0f : 15.0f;
+  int u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    u[i] = affine_code_inv(x[i], sc, inv, mn, levels);
+    x[i] = fmaf((float)u[i], s, z);
+  }
+  if (!live) return;
+  if (bits == 8) {
+    uint2 w;
+    w.x = (u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24)) ^ 0x80808080u;
+    w.y = (u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24)) ^ 0x80808080u;
+    *reinterpret_cast<uint2*>(dst) = w;
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= (uint32_t)u[i] << (4 * i);
+    *reinterpret_cast<uint32_t*>(dst) = w;
+  }
+}
+
+// store_row for a lane's two runs of eight channels; l: the lane's place in its row.
+template <int D>
+__device__ __forceinline__ void store_chunks(const PoolSide& s, size_t row, int l, bool live, float (&x)[16]) {
+  uint8_t* codes = s.codes + row * s.row_bytes;
+  if (s.bits == 16) {
+    const Eight<__half> lo = pack8<__half>(x), hi = pack8<__half>(x + 8);
+    if (live) {
+      lo.store(reinterpret_cast<__half*>(codes) + 8 * l);
+      hi.store(reinterpret_cast<__half*>(codes) + D / 2 + 8 * l);
+    }
+    unpack8<__half>(lo, x);
+    unpack8<__half>(hi, x + 8);
+    return;
+  }
+  float mn[2] = {x[0], x[8]}, mx[2] = {x[0], x[8]};
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    mn[0] = fminf(mn[0], x[i]);
+    mx[0] = fmaxf(mx[0], x[i]);
+    mn[1] = fminf(mn[1], x[8 + i]);
+    mx[1] = fmaxf(mx[1], x[8 + i]);
+  }
+  if (s.group == D) {   // one group: both runs
+    mn[0] = mn[1] = fminf(mn[0], mn[1]);
+    mx[0] = mx[1] = fmaxf(mx[0], mx[1]);
+  }
+  const int width = min(s.group, D / 2) / 8;   // lanes that share a group
+#pragma unroll
+  for (int o = 1; o < D / 16; o <<= 1) {
+    if (o < width) {   // the same for every lane
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mn[i] = fminf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], o));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+      }
+    }
+  }
+  const float levels = s.bits == 8 ? 255.0f : 15.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float sc = affine_scale(mn[i], mx[i], levels);
+    const __half s16 = __float2half_rn(sc), z16 = __float2half_rn(mn[i]);
+    const int c = i * (D / 2) + 8 * l;
+    code_eight(codes + c * s.bits / 8, s.bits, x + 8 * i, sc, __frcp_rn(sc), mn[i], __half2float(s16),
+               __half2float(z16), live);
+    if (live && l % width == 0 && !(i && s.group == D)) s.meta[row * s.n_groups + c / s.group] = __halves2half2(s16, z16);
+  }
+}
+
+// A warp takes one token and `rows_per_warp` groups of 32 / (D / 16) head rows;
+// groups never mix queries, keys and values.
+template <int D, typename T, bool PAGED>
+__global__ void __launch_bounds__(32 * kRowWarps) token_chunks_kernel(const __grid_constant__ TokenArgs a) {
+  constexpr int L = D / 16;     // lanes per row
+  constexpr int R = 32 / L;     // rows per group
+  constexpr int U = 2;          // groups loaded before the first is used
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, l = lane % L, rg = lane / L;
+  const long long job = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const int tok = (int)(job / a.slices);
+  if (tok >= a.n_tokens) return;
+  const int gq = (a.q.heads + R - 1) / R, gk = (a.k.heads + R - 1) / R;
+  const int total = gq + gk + (PAGED ? gk : 0);
+  const int g0 = (int)(job % a.slices) * a.rows_per_warp;
+  const int g1 = min(g0 + a.rows_per_warp, total);
+  if (g0 >= g1) return;
+
+  int pos = 0;
+  long long page_row = -1;
+  if constexpr (PAGED) {
+    int b = tok, j = 0, n = 1;
+    if (a.cu) {
+      b = sequence_of(a.cu, a.batch.n_seqs, tok, lane);
+      if (b < 0) return;
+      j = tok - a.cu[b];
+      n = a.cu[b + 1] - a.cu[b];
+    }
+    const long long at = (long long)a.batch.lens[b] - n + j;
+    if (at < 0) return;
+    pos = (int)at + (a.batch.prefix_len ? max(a.batch.prefix_len[0], 0) : 0);
+    if (g1 > gq) {
+      const long long col = at >> a.page_log2;
+      const int id = col < a.batch.max_pages ? a.batch.table[(long long)b * a.batch.max_pages + col] : -1;
+      if ((unsigned)id < (unsigned)a.n_pages)
+        page_row = (((long long)id * a.Hkv) << a.page_log2) + (at & ((1 << a.page_log2) - 1));
+      else if (lane == 0)
+        set_pool_status(a.status, KVQ_DEV_BAD_PAGE);
+    }
+  }
+  if (a.positions) pos = a.positions[tok];
+
+  // sines (of each pair's first channel) and cosines of the lane's eight pairs
+  float cs[8], sn[8];
+  int pairing = kStraight;
+  if (a.rope.freqs && g0 < gq + gk) {
+    const bool inter = a.rope.interleaved != 0;
+    pairing = inter ? kNeighbours : (a.rope.rot == D ? kHalves : kQuarter);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // the pair's first channel and its index
+      const int c = inter ? (i < 4 ? 0 : D / 2) + 8 * l + 2 * (i & 3) : 8 * l + i;
+      const int p = inter ? c >> 1 : (pairing == kQuarter && c >= D / 4 ? c - D / 4 : c);
+      cs[i] = 1.0f;
+      sn[i] = 0.0f;
+      if (!inter || c < a.rope.rot) {
+        const long long turn = (long long)((unsigned long long)(long long)pos * a.rope.freqs[p]);
+        float s, co;
+        sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &co);
+        cs[i] = co * a.rope.mag;
+        sn[i] = (pairing == kQuarter && c >= D / 4 ? s : -s) * a.rope.mag;   // kQuarter: the lane's own sign
+      }
+    }
+  }
+
+  auto view = [&](int g, int& h, int& kind) -> const RowsView& {
+    kind = g < gq ? 0 : (g < gq + gk ? 1 : 2);
+    h = (g - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * R + rg;
+    return kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+  };
+  for (int g = g0; g < g1; g += U) {
+    Eight<T> lo[U], hi[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (g + i < g1) {
+        int h, kind;
+        const RowsView& w = view(g + i, h, kind);
+        if (h >= w.heads) h = w.heads - 1;   // a group's spare lanes repeat the last row and store nothing
+        const T* p = static_cast<const T*>(w.in) + tok * w.in_tok + h * w.in_head + 8 * l;
+        lo[i].load(p);
+        hi[i].load(p + D / 2);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (g + i < g1) {
+        int h, kind;
+        const RowsView& w = view(g + i, h, kind);
+        const bool mine = h < w.heads;
+        if (!mine) h = w.heads - 1;
+        float x[16];
+        unpack8<T>(lo[i], x);
+        unpack8<T>(hi[i], x + 8);
+        if (!PAGED || kind < 2) {
+          if (w.weight) {
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              s0 = fmaf(x[e], x[e], s0);
+              s1 = fmaf(x[8 + e], x[8 + e], s1);
+            }
+            s0 += s1;
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+            const float inv = 1.0f / sqrtf(s0 * (1.0f / D) + a.eps);
+            Eight<T> wl, wh;
+            const T* wt = static_cast<const T*>(w.weight) + 8 * l;
+            wl.load(wt);
+            wh.load(wt + D / 2);
+            float f[16];
+            unpack8<T>(wl, f);
+            unpack8<T>(wh, f + 8);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * f[e];
+          }
+          if (pairing == kHalves) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p = x[e], q = x[8 + e];
+              x[e] = fmaf(q, sn[e], p * cs[e]);
+              x[8 + e] = fmaf(p, -sn[e], q * cs[e]);
+            }
+          } else if (pairing == kNeighbours) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p = x[2 * e], q = x[2 * e + 1];
+              x[2 * e] = fmaf(q, sn[e], p * cs[e]);
+              x[2 * e + 1] = fmaf(p, -sn[e], q * cs[e]);
+            }
+          } else if (pairing == kQuarter) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float o = __shfl_xor_sync(0xffffffffu, x[e], L / 2);
+              x[e] = fmaf(o, sn[e], x[e] * cs[e]);
+            }
+          }
+        }
+        if (PAGED && kind > 0)
+          store_chunks<D>(kind == 1 ? a.ks : a.vs, (size_t)(page_row < 0 ? 0 : page_row + ((long long)h << a.page_log2)),
+                          l, mine && page_row >= 0, x);
+        if (mine && (!PAGED || kind == 0 || w.out)) {
+          T* o = static_cast<T*>(w.out) + tok * w.out_tok + h * w.out_head + 8 * l;
+          pack8<T>(x).store(o);
+          pack8<T>(x + 8).store(o + D / 2);
+        }
+      }
+    }
+  }
+}
+
+template <typename K>
+cudaError_t launch_rows(K kernel, const TokenArgs& a, unsigned grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(32 * kRowWarps);
@@ -306,27 +610,37 @@ cudaError_t launch_typed(const TokenArgs& a, bool paged, unsigned grid, cudaStre
   cfg.attrs = at;
   cfg.numAttrs = 1;
   note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int E, typename T>
+cudaError_t launch_typed(const TokenArgs& a, bool paged, bool chunks, unsigned grid, cudaStream_t st) {
+  constexpr int D = 32 * E;
   if constexpr (E == 2 || E == 4) {
-    if (paged) return cudaLaunchKernelEx(&cfg, token_rows_kernel<E, T, true>, a);
+    if (paged) return chunks ? launch_rows(token_chunks_kernel<D, T, true>, a, grid, st)
+                             : launch_rows(token_rows_kernel<E, T, true>, a, grid, st);
   }
-  return cudaLaunchKernelEx(&cfg, token_rows_kernel<E, T, false>, a);
+  if constexpr (E > 1) {
+    if (chunks) return launch_rows(token_chunks_kernel<D, T, false>, a, grid, st);
+  }
+  return launch_rows(token_rows_kernel<E, T, false>, a, grid, st);
 }
 
 template <int E>
-cudaError_t launch_dim(const TokenArgs& a, int dtype, bool paged, unsigned grid, cudaStream_t st) {
-  if (dtype == KVQ_DTYPE_F32) return launch_typed<E, float>(a, paged, grid, st);
-  if (dtype == KVQ_DTYPE_BF16) return launch_typed<E, __nv_bfloat16>(a, paged, grid, st);
-  return launch_typed<E, __half>(a, paged, grid, st);
+cudaError_t launch_dim(const TokenArgs& a, int dtype, bool paged, bool chunks, unsigned grid, cudaStream_t st) {
+  if (dtype == KVQ_DTYPE_F32) return launch_typed<E, float>(a, paged, chunks, grid, st);
+  if (dtype == KVQ_DTYPE_BF16) return launch_typed<E, __nv_bfloat16>(a, paged, chunks, grid, st);
+  return launch_typed<E, __half>(a, paged, chunks, grid, st);
 }
 
-// Whole-lane vector accesses need every row start of `w` on the lane's vector size.
+// Vector accesses of vec_bytes need every row start of `w` (and its weights) on that boundary.
 bool rows_aligned(const RowsView& w, int elem, int vec_bytes) {
   if (!w.heads) return true;
   const int n = vec_bytes / elem;   // elements per vector
   auto ok = [&](const void* p, long long ts, long long hs) {
     return !p || ((reinterpret_cast<uintptr_t>(p) % vec_bytes) == 0 && ts % n == 0 && hs % n == 0);
   };
-  return ok(w.in, w.in_tok, w.in_head) && ok(w.out, w.out_tok, w.out_head);
+  return ok(w.in, w.in_tok, w.in_head) && ok(w.out, w.out_tok, w.out_head) && ok(w.weight, 0, 0);
 }
 
 }  // namespace
@@ -334,24 +648,33 @@ bool rows_aligned(const RowsView& w, int elem, int vec_bytes) {
 cudaError_t launch_token_rows(const TokenArgs& args, int D, int dtype, bool paged, int sms, cudaStream_t st) {
   TokenArgs a = args;
   const int elem = dtype == KVQ_DTYPE_F32 ? 4 : 2;
+  auto all_aligned = [&](int bytes) {
+    return rows_aligned(a.q, elem, bytes) && rows_aligned(a.k, elem, bytes) && rows_aligned(a.v, elem, bytes);
+  };
+  // sixteen channels a lane: whole heads, half heads of the half layout, or any interleaved run
+  const bool chunks = D >= 64 && all_aligned(16) &&
+                      (!a.rope.freqs || a.rope.interleaved || a.rope.rot == D || a.rope.rot == D / 2);
   const int lane_bytes = D / 32 * elem;
-  const int vb = lane_bytes > 16 ? 16 : lane_bytes;
-  a.vec = rows_aligned(a.q, elem, vb) && rows_aligned(a.k, elem, vb) && rows_aligned(a.v, elem, vb);
-  const int total = a.q.heads + a.k.heads + (paged ? a.v.heads : 0);
+  a.vec = all_aligned(lane_bytes > 16 ? 16 : lane_bytes);
+  // units of work of a token: rows, or groups of rows
+  const int R = chunks ? 512 / D : 1;
+  auto units = [&](int heads) { return (heads + R - 1) / R; };
+  const int total = units(a.q.heads) + units(a.k.heads) + (paged ? units(a.v.heads) : 0);
   // Few tokens: one load batch a warp, for the most warps.  Once the tokens
-  // alone give every SM its 64 warps twice over, a warp takes 16 rows, so that
-  // the sines are computed once for more rows.
-  a.rows_per_warp = (long long)a.n_tokens * ((total + 15) / 16) >= 128LL * sms ? 16 : kRowUnroll;
+  // give every SM its 64 warps twice over, a warp takes more, so that the
+  // sines are computed once for more rows.
+  const int few = chunks ? 2 : kRowUnroll, many = 16;
+  a.rows_per_warp = (long long)a.n_tokens * ((total + many - 1) / many) >= 128LL * sms ? many : few;
   if (a.rows_per_warp > total) a.rows_per_warp = total;
   a.slices = (total + a.rows_per_warp - 1) / a.rows_per_warp;
   const long long jobs = (long long)a.n_tokens * a.slices;
   const long long grid = (jobs + kRowWarps - 1) / kRowWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   switch (D) {
-    case 32: return launch_dim<1>(a, dtype, paged, (unsigned)grid, st);
-    case 64: return launch_dim<2>(a, dtype, paged, (unsigned)grid, st);
-    case 128: return launch_dim<4>(a, dtype, paged, (unsigned)grid, st);
-    default: return launch_dim<8>(a, dtype, paged, (unsigned)grid, st);
+    case 32: return launch_dim<1>(a, dtype, paged, chunks, (unsigned)grid, st);
+    case 64: return launch_dim<2>(a, dtype, paged, chunks, (unsigned)grid, st);
+    case 128: return launch_dim<4>(a, dtype, paged, chunks, (unsigned)grid, st);
+    default: return launch_dim<8>(a, dtype, paged, chunks, (unsigned)grid, st);
   }
 }
 
