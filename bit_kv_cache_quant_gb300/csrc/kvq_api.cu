@@ -74,6 +74,8 @@ namespace {
 
 thread_local std::string g_err;
 thread_local int g_launches = 0;
+// kvq_test_stall_decode_tiles: bytes every decode CTA's first tile barrier expects in excess.
+std::atomic<unsigned> g_stall_tx{0};
 
 kvq_status fail(kvq_status s, const char* fmt, ...) {
   char buf[512];
@@ -331,6 +333,8 @@ size_t live_bytes(const kvq_cache_s* c, int stored) {
 
 void kvq::note_launch(int n) { g_launches += n; }
 
+unsigned kvq::test_stall_bytes() { return g_stall_tx.load(std::memory_order_relaxed); }
+
 kvq_status kvq::report_error(kvq_status s, const char* msg) {
   begin_call();
   return fail(s, "%s", msg);
@@ -516,8 +520,6 @@ kvq_status kvq_decode_plan_query(const kvq_config* cfg, int32_t n_q_heads, int32
 
 namespace {
 
-// kvq_test_stall_decode_tiles: bytes every decode CTA's first tile barrier expects in excess.
-std::atomic<unsigned> g_stall_tx{0};
 
 // Argument checks shared by kvq_decode_attn and kvq_append_decode.
 kvq_status check_decode_args(kvq_cache c, const void* q, void* out, int32_t n_q_heads, int32_t io_dtype,

@@ -10,6 +10,9 @@ namespace kvq {
 // the row length; false when the driver cannot encode it (kvq_api.cu).
 bool encode_rows_map(CUtensorMap* m, void* base, size_t rows, int row_bytes, int box_rows);
 
+// The test hook of kvq_test_stall_decode_tiles: bytes a CTA's first barrier expects in excess.
+unsigned test_stall_bytes();
+
 // One tensor of a token-row launch, strides in elements.
 struct RowsView {
   const void* in;

@@ -402,6 +402,12 @@ kvq_status kvq_paged_decode_attn(kvq_paged pool, const kvq_paged_batch* batch, c
   if (n_q_heads < 1 || n_q_heads % hkv)
     return fail(KVQ_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
   if (n_q_heads / hkv > 8) return fail(KVQ_ERR_UNSUPPORTED, "more than 8 query heads per kv head");
+  // rows, and the tiles of 64 rows of every (sequence, kv head), are counted in 32 bits
+  const int64_t cols = (int64_t)batch->max_pages + batch->max_prefix_pages;
+  const int64_t tiles = (cols * pool->cfg.page_size + 63) / 64 + 1;
+  if (cols * pool->cfg.page_size >= INT32_MAX - 128 || tiles > INT32_MAX / batch->n_seqs / hkv)
+    return fail(KVQ_ERR_UNSUPPORTED, "n_seqs * n_kv_heads * (max_pages + max_prefix_pages) * page_size / 64 must stay "
+                                     "below 2^31, and a sequence's rows below 2^31 - 128");
   const size_t need = kvq::paged_workspace_bytes(pool->view, batch->n_seqs, n_q_heads, batch->max_prefix_pages);
   if (ws_bytes < need) return fail(KVQ_ERR_CAPACITY, "workspace holds %zu bytes, the call needs %zu", ws_bytes, need);
   a.q = q;

@@ -1,109 +1,131 @@
-// Decode attention over a page pool: one query token per sequence, over a
-// prefix shared by the batch and each sequence's own pages.
-//
-// One CTA per (sequence, query head); its warps take rows in turn, lane l the
-// channels [l E, l E + E), and keep their own online-softmax state, merged at
-// the end.  Every sequence reads the prefix for itself.
-#include "paged.cuh"
+// Launch of paged decode attention: the streaming kernel (paged_own.cuh) and
+// the merge of the states of units that span CTAs.
+#include "paged_own.cuh"
 
 namespace kvq {
 
 namespace {
 
-constexpr int kWarps = 4;
-
-template <int E>
-__device__ __forceinline__ void load_values(const PoolSide& s, size_t row, int lane, float (&x)[E]) {
-  const uint8_t* p = s.codes + row * s.row_bytes;
-  if (s.bits == 16) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __half2float(reinterpret_cast<const __half*>(p)[lane * E + e]);
-    return;
+// Joins a unit's states with the online-softmax rule, one warp per query
+// head.  A unit that one CTA finished is left alone; one without rows gets
+// zeros.
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, int Hkv, int grid) {
+  constexpr int C = D / 32;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
+  const int unit = blockIdx.x, b = unit / Hkv, kvh = unit - b * Hkv;
+  const long long total = (long long)a.starts[a.batch.n_seqs] * Hkv;
+  const int tiles = a.starts[b + 1] - a.starts[b];
+  const long long x0 = (long long)a.starts[b] * Hkv + (long long)kvh * tiles, x1 = x0 + tiles - 1;
+  const int ctas = busy_ctas(total, grid);
+  int c0 = 0, n = 0;
+  if (tiles > 0) {   // CTA c takes the tiles from total * c / ctas on
+    c0 = (int)(((x0 + 1) * ctas + total - 1) / total) - 1;
+    n = (int)(((x1 + 1) * ctas + total - 1) / total) - c0;
   }
-  const float2 m = __half22float2(s.meta[row * s.n_groups + lane * E / s.group]);
+  if (n == 1 && !a.joined) return;
+  const float* own = a.parts + ((size_t)(c0 + unit) * a.G + h) * (D + kPartPad);
+  const size_t stride = (size_t)a.G * (D + kPartPad);
+  float m = neg_inf();
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, own[i * stride + D]);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = lane * E + e;
-    const int u = s.bits == 8 ? p[c] ^ 0x80 : (p[c >> 1] >> (4 * (c & 1))) & 15;
-    x[e] = fmaf((float)u, m.x, m.y);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.0f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* s = own + i * stride;
+    const float li = s[D + 1];
+    const float w = li == 0.0f ? 0.0f : fast_exp2(s[D] - m);
+    float x[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c] = s[lane * C + c];
+    l = fmaf(li, w, l);
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = fmaf(w, x[c], acc[c]);
   }
+  const float r = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t at = ((size_t)b * a.Hq + (size_t)kvh * a.G + h) * D + lane * C;
+#pragma unroll
+  for (int c = 0; c < C; ++c) store_io(a.out, at + c, a.io_dtype, acc[c] * r);
 }
 
-template <int E>
-__global__ void __launch_bounds__(32 * kWarps) paged_decode_kernel(const __grid_constant__ PoolView p,
-                                                                   const PagedDecodeArgs a) {
-  constexpr int D = 32 * E;
-  __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int kvh = h / (a.Hq / p.Hkv);
-  const size_t qo = ((size_t)b * a.Hq + h) * D + lane * E;
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = load_io(a.q, qo + e, a.io_dtype) * a.qscale;
-    o[e] = 0.0f;
-  }
-  for (int part = 0; part < 2; ++part) {
-    const int* pages = part ? a.batch.table + (size_t)b * a.batch.max_pages : a.batch.prefix_pages;
-    const int cols = part ? a.batch.max_pages : a.batch.max_prefix_pages;
-    long long n = part ? a.batch.lens[b] : (a.batch.max_prefix_pages ? a.batch.prefix_len[0] : 0);
-    if (n > ((long long)cols << p.page_log2)) {
-      n = (long long)cols << p.page_log2;
-      if (threadIdx.x == 0) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
-    }
-    for (int j = warp; j < n; j += kWarps) {
-      const int id = pages[j >> p.page_log2];
-      if ((unsigned)id >= (unsigned)p.n_pages) {
-        if (lane == 0) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
-        continue;
-      }
-      const size_t row = ((((size_t)id * p.Hkv) + kvh) << p.page_log2) + (j & (p.page - 1));
-      float k[E], v[E], s = 0.0f;
-      load_values<E>(p.k, row, lane, k);
-      load_values<E>(p.v, row, lane, v);
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-      const float mn = fmaxf(m, s);
-      const float al = exp2f(m - mn), pr = exp2f(s - mn);
-      l = l * al + pr;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(pr, v[e], o[e] * al);
-      m = mn;
-    }
-  }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
-    float mm = -INFINITY, ll = 0.0f, oo = 0.0f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w]);
-    for (int w = 0; w < kWarps; ++w) {
-      if (sm_l[w] == 0.0f) continue;
-      const float f = exp2f(sm_m[w] - mm);
-      ll = fmaf(sm_l[w], f, ll);
-      oo = fmaf(sm_o[w][d], f, oo);
-    }
-    store_io(a.out, ((size_t)b * a.Hq + h) * D + d, a.io_dtype, ll > 0.0f ? oo / ll : 0.0f);
-  }
+size_t starts_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * 4 + 255) / 256 * 256; }
+
+template <int D, int F, int HG>
+cudaError_t launch_own(const PoolView& p, OwnArgs a, int max_tiles_per_seq, cudaStream_t st) {
+  using S = OwnShape<D, F, HG>;
+  auto kern = paged_own_kernel<D, F, HG>;
+  const int base = S::kStages * S::kStage + S::kAcc + 1024;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = once_per_device(configured, [&]() {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, base + 4097 * 4);
+  });
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)a.batch.n_seqs * p.Hkv * max_tiles_per_seq;   // tiles, at most
+  long long ctas = (long long)S::kCtas * p.sms;
+  if (ctas > most) ctas = most < 1 ? 1 : most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = base + (a.batch.n_seqs + 1) * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p, a);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  cfg.gridDim = dim3(a.batch.n_seqs * p.Hkv);
+  cfg.blockDim = dim3(32 * a.G);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, (const OwnArgs)a, p.Hkv, (int)ctas);
+  note_launch();
+  return e;
+}
+
+template <int D, int F>
+cudaError_t launch_heads(const PoolView& p, const OwnArgs& a, int max_tiles, cudaStream_t st) {
+  return a.G <= 4 ? launch_own<D, F, 1>(p, a, max_tiles, st) : launch_own<D, F, 2>(p, a, max_tiles, st);
+}
+
+template <int D>
+cudaError_t launch_format(const PoolView& p, const OwnArgs& a, int max_tiles, cudaStream_t st) {
+  if (p.k.bits == 16) return launch_heads<D, F_FP16>(p, a, max_tiles, st);
+  if (p.k.bits == 8) return launch_heads<D, F_AFF8>(p, a, max_tiles, st);
+  return launch_heads<D, F_AFF4>(p, a, max_tiles, st);
 }
 
 }  // namespace
 
-size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_prefix_pages) { return 16; }
+size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_prefix_pages) {
+  (void)max_prefix_pages;
+  const size_t states = (size_t)4 * p.sms + (size_t)n_seqs * p.Hkv;
+  return starts_bytes(n_seqs) + states * (Hq / p.Hkv) * (p.D + kPartPad) * sizeof(float);
+}
 
-cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& a, cudaStream_t st) {
-  const dim3 grid(a.Hq, a.batch.n_seqs);
-  note_launch();
-  if (p.D == 64) paged_decode_kernel<2><<<grid, 32 * kWarps, 0, st>>>(p, a);
-  else paged_decode_kernel<4><<<grid, 32 * kWarps, 0, st>>>(p, a);
-  return cudaGetLastError();
+cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& d, cudaStream_t st) {
+  OwnArgs a{};
+  a.batch = d.batch;
+  a.q = d.q;
+  a.out = d.out;
+  a.starts = reinterpret_cast<int*>(d.ws);
+  a.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(d.ws) + starts_bytes(d.batch.n_seqs));
+  a.io_dtype = d.io_dtype;
+  a.Hq = d.Hq;
+  a.G = d.Hq / p.Hkv;
+  a.qscale = d.qscale;
+  a.with_prefix = d.batch.max_prefix_pages > 0;
+  a.joined = 0;
+  a.stall_tx = test_stall_bytes();
+  auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 63) >> 6); };
+  const int max_tiles = tiles(d.batch.max_pages) + tiles(d.batch.max_prefix_pages);
+  return p.D == 64 ? launch_format<64>(p, a, max_tiles, st) : launch_format<128>(p, a, max_tiles, st);
 }
 
 }  // namespace kvq

@@ -1,0 +1,589 @@
+// Paged decode attention, the streaming part: every (sequence, kv head) with
+// its own rows (and, where the prefix is not worth a launch of its own, the
+// prefix rows in front of them).
+//
+// Work is cut by tiles of 64 rows, not by sequences: the tiles of all units
+// (sequence, kv head) stand in one line, CTA c of n takes those from
+// c * total / n on, and a unit that spans CTAs is joined by the merge kernel
+// from one partial state per (CTA, unit).  A ragged batch thus loads every SM
+// alike, whatever its lengths.  A CTA's tile range is found from a scan of
+// the lengths, which every CTA does for itself.
+//
+// One warp copies: lane i looks up the pages of the CTA's i-th next tile, so
+// that the table's latency is paid once per 32 tiles, and issues that tile's
+// copies (codes by TMA with the swizzle of the row length, metadata and the
+// unit's query rows by bulk copies) when its stage is free.  Four warps per
+// four query heads compute, 16 rows of a tile each, with the arithmetic of
+// the contiguous cache's decode (decode_tc.cuh): transposed products on
+// mma.sync m16n8k16 with 16 rows of keys or channels of values on the wide
+// side and four heads as (fp16 part, residual) pairs on the narrow one, keys
+// as exact integer codes with one fp32 accumulator per 32 channels.
+// A page holds whole 16-row blocks, so a block is on one page: a bad page id
+// takes its blocks out.
+//
+// Bound by HBM: 16 to 64 query rows per tile leave the tensor pipe idle.
+#pragma once
+
+#include "decode_tc.cuh"
+#include "paged.cuh"
+
+namespace kvq {
+
+constexpr int kPartPad = 4;   // partial row: D accumulators, max, sum, 2 pad
+
+// Tiles of 64 rows of a part of `len` rows behind `cols` page-table entries (its length cut to them).
+struct Part {
+  int len, tiles;
+};
+__device__ __forceinline__ Part part_of(int len, int cols, int page_log2, int* status) {
+  long long room = (long long)cols << page_log2;
+  Part p;
+  p.len = max(len, 0);
+  if (p.len > room) {
+    p.len = (int)room;
+    if (status) set_pool_status(status, KVQ_DEV_BAD_PAGE);
+  }
+  p.tiles = (p.len + 63) >> 6;
+  return p;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* m) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(m)) : "memory");
+}
+// Barrier `id` over `threads` threads of the CTA.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// CTAs of a grid that share `total` tiles: every one of them has some.
+__device__ __forceinline__ int busy_ctas(long long total, int grid) { return (int)(total < grid ? total : grid); }
+
+template <int D, int F, int HG> struct OwnShape {
+  static constexpr int kBits = FmtBits<F>::v;
+  static constexpr int kRow = D * kBits / 8;
+  static constexpr bool kAff = F != F_FP16;
+  static constexpr int kNgMax = kAff ? D / 32 : 0;
+  static constexpr int kCodes = 64 * kRow;
+  static constexpr int kMeta = 64 * kNgMax * 4;
+  static constexpr int kQ = 4 * HG * D * 2;
+  static constexpr int kStage = (2 * kCodes + 2 * kMeta + kQ + 1023) / 1024 * 1024;
+  static constexpr int kWarps = 4 * HG;            // computing warps
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kAcc = kWarps * 4 * (D + 8) * 4;   // the warps' states at a unit's end
+  // CTAs per SM: as many as keep three stages each; four at most (registers)
+  static constexpr int kCtas = HG > 1 ? 2 : (kStage > 24 * 1024 ? 2 : (kStage > 12 * 1024 ? 3 : 4));
+  static constexpr int kRaw = (225 * 1024 / kCtas - 4096 - kAcc) / kStage;
+  static constexpr int kStages = kRaw < 2 ? 2 : (kRaw > 8 ? 8 : kRaw);
+};
+
+struct OwnArgs {
+  BatchView batch;
+  const void* q;
+  void* out;
+  float* parts;      // [grid + n_seqs * Hkv] states of [G][D + kPartPad]
+  int* starts;       // [n_seqs + 1] tiles of one kv head in front of each sequence, for the merge
+  int io_dtype;
+  int Hq, G;
+  float qscale;
+  int with_prefix;   // the units' rows begin with the prefix's
+  int joined;        // further states come from elsewhere: no unit is final here
+  unsigned stall_tx; // test hook, as DecodeArgs
+};
+
+template <int D, int F, int HG>
+__global__ void __launch_bounds__(OwnShape<D, F, HG>::kThreads, OwnShape<D, F, HG>::kCtas)
+    paged_own_kernel(const __grid_constant__ PoolView p, const __grid_constant__ OwnArgs a) {
+  using S = OwnShape<D, F, HG>;
+  constexpr int KB = S::kBits, ROW = S::kRow, NST = S::kStages, NCW = S::kWarps;
+  constexpr int KS = D / 16, NB = D / 32, MT = D / 16, VCH = D / 8, VTB = ROW / 8;
+  constexpr bool AFF = S::kAff;
+  constexpr int NACC = AFF ? NB : 1;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float(*sm_acc)[4][D + 8] = reinterpret_cast<float(*)[4][D + 8]>(smem + NST * S::kStage);
+  int* sm_start = reinterpret_cast<int*>(smem + NST * S::kStage + S::kAcc);   // [n_seqs + 1]
+  __shared__ __align__(8) uint64_t full[NST], empty[NST];
+  __shared__ float sm_m[NCW][4], sm_l[NCW][4];
+  __shared__ int s_bad[NST], s_issued[NST], s_scan[NCW + 1];
+  __shared__ volatile int s_fail;
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    s_fail = 0;
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NCW);
+      s_issued[s] = -1;
+    }
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- tiles in front of each sequence (of one kv head)
+  const int n = a.batch.n_seqs;
+  const bool lead = blockIdx.x == 0;
+  Part pre{0, 0};
+  if (a.with_prefix) pre = part_of(a.batch.prefix_len[0], a.batch.max_prefix_pages, p.page_log2, lead ? p.status : nullptr);
+  {
+    const int per = (n + S::kThreads - 1) / S::kThreads;
+    const int i0 = min(threadIdx.x * per, n), i1 = min(i0 + per, n);
+    int sum = 0;
+    for (int i = i0; i < i1; ++i)
+      sum += pre.tiles + part_of(a.batch.lens[i], a.batch.max_pages, p.page_log2, lead ? p.status : nullptr).tiles;
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    int at = inc - sum;
+    for (int w = 0; w < warp; ++w) at += s_scan[w];
+    for (int i = i0; i < i1; ++i) {
+      sm_start[i] = at;
+      at += pre.tiles + part_of(a.batch.lens[i], a.batch.max_pages, p.page_log2, nullptr).tiles;
+    }
+    if (threadIdx.x == 0) {
+      int all = 0;
+      for (int w = 0; w <= NCW; ++w) all += s_scan[w];
+      sm_start[n] = all;
+    }
+    __syncthreads();
+    if (lead)
+      for (int i = threadIdx.x; i <= n; i += S::kThreads) a.starts[i] = sm_start[i];
+  }
+  const long long total = (long long)sm_start[n] * p.Hkv;
+  const int ctas = busy_ctas(total, gridDim.x);
+  if (blockIdx.x >= ctas) return;
+  const long long t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
+  const int ntile = (int)(t1 - t0);   // at least one
+
+  // Sequence, kv head and tile of the unit that tile x of the line belongs to.
+  struct At {
+    int b, kvh, j, tiles;
+  };
+  auto locate = [&](long long x) {
+    int lo = 0, hi = n;   // the last b with sm_start[b] * Hkv <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)sm_start[mid] * p.Hkv <= x) lo = mid;
+      else hi = mid;
+    }
+    At r;
+    r.b = lo;
+    r.tiles = sm_start[lo + 1] - sm_start[lo];
+    const int rest = (int)(x - (long long)sm_start[lo] * p.Hkv);
+    r.kvh = rest / r.tiles;
+    r.j = rest - r.kvh * r.tiles;
+    return r;
+  };
+
+  const int kng = p.k.n_groups, vng = p.v.n_groups;
+  if (warp == NCW) {
+    // ------------------------------------------------------------- copies
+    for (int base = 0; base < ntile && !s_fail; base += 32) {
+      const bool mine = base + lane < ntile;
+      int ids[4] = {-1, -1, -1, -1}, kvh = 0, b = 0, off = 0, np = 0;
+      bool first = false;
+      if (mine) {
+        const At u = locate(t0 + base + lane);
+        b = u.b;
+        kvh = u.kvh;
+        const bool in_pre = u.j < pre.tiles;
+        const int j = in_pre ? u.j : u.j - pre.tiles;
+        const int len = in_pre ? pre.len : part_of(a.batch.lens[b], a.batch.max_pages, p.page_log2, nullptr).len;
+        const int* pages = in_pre ? a.batch.prefix_pages : a.batch.table + (size_t)b * a.batch.max_pages;
+        const int rows = min(64, len - j * 64);
+        np = p.page_log2 >= 6 ? 1 : (rows + (1 << p.page_log2) - 1) >> p.page_log2;
+        off = (j * 64) & ((1 << p.page_log2) - 1);
+        first = u.j == 0 || base + lane == 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < np) ids[i] = pages[((j * 64) >> p.page_log2) + i];
+      }
+      const int cnt = min(32, ntile - base);
+      for (int s = 0; s < cnt; ++s) {
+        const int it = base + s, stg = it % NST;
+        if (it >= NST) {
+          if (s_fail || !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[stg], ((it / NST) - 1) & 1))) {
+            s_fail = 1;
+            break;
+          }
+        }
+        if (lane == s) {
+          if (it >= NST) fence_async_smem();   // the stage's readers are done: order the copies behind them
+          uint8_t* st = smem + stg * S::kStage;
+          const int rows = min(64, 1 << p.page_log2);   // of one copy
+          int bad = 0, good = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i < np) {
+              if ((unsigned)ids[i] < (unsigned)p.n_pages) ++good;
+              else bad |= ((1 << (rows >> 4)) - 1) << (i * (rows >> 4));
+            }
+          }
+          if (bad) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
+          s_bad[stg] = bad;
+          s_issued[stg] = (it / NST) & 1;
+          const uint32_t qb = first ? (uint32_t)(a.G * D * 2) : 0u;
+          mbar_expect_tx(&full[stg], (uint32_t)(good * rows * (2 * ROW + 4 * (kng + vng))) + qb +
+                                         (it == 0 ? a.stall_tx : 0u));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i < np && (unsigned)ids[i] < (unsigned)p.n_pages) {
+              const int row = (int)((((long long)ids[i] * p.Hkv + kvh) << p.page_log2) + off);
+              uint8_t* dk = st + i * rows * ROW;
+              if constexpr (ROW == 256) {
+                tma_rows<256>(dk, &p.kmap, row, &full[stg]);
+                tma_rows<256>(dk + S::kCodes, &p.vmap, row, &full[stg]);
+              } else {
+                tma_rows<ROW>(dk, &p.kmap, row, &full[stg]);
+                tma_rows<ROW>(dk + S::kCodes, &p.vmap, row, &full[stg]);
+              }
+              if constexpr (AFF) {
+                bulk_copy(st + 2 * S::kCodes + i * rows * 4 * kng, p.k.meta + (size_t)row * kng,
+                          (uint32_t)(rows * 4 * kng), &full[stg]);
+                bulk_copy(st + 2 * S::kCodes + S::kMeta + i * rows * 4 * vng, p.v.meta + (size_t)row * vng,
+                          (uint32_t)(rows * 4 * vng), &full[stg]);
+              }
+            }
+          }
+          if (first)
+            bulk_copy(st + 2 * S::kCodes + 2 * S::kMeta,
+                      static_cast<const uint16_t*>(a.q) + ((size_t)b * a.Hq + (size_t)kvh * a.G) * D, qb, &full[stg]);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- products
+    const int g = lane >> 2, t = lane & 3;
+    const int hg = warp >> 2, blk = (warp & 3) * 16;
+    const int hd = 4 * hg + t;
+    const int rk[2] = {blk + tau<ROW>(g), blk + tau<ROW>(g + 8)};
+    const int rr[4] = {blk + tau<ROW>(2 * t), blk + tau<ROW>(2 * t + 1), blk + tau<ROW>(2 * t + 8),
+                       blk + tau<ROW>(2 * t + 9)};
+    const int vgi = AFF ? (g * VCH) / p.v.group : 0;
+    const bool vfold = AFF && vng == 1;
+    float m_run = neg_inf(), l_part = 0.0f, zacc = 0.0f;
+    float oacc[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) oacc[mt][0] = oacc[mt][1] = oacc[mt][2] = oacc[mt][3] = 0.0f;
+    uint32_t qf[KS][2];
+    float qg[NB];
+    At u = locate(t0);
+    bool first = true, begun_here = u.j == 0;
+    int own_len = part_of(a.batch.lens[u.b], a.batch.max_pages, p.page_log2, nullptr).len;
+
+    for (int it = 0; it < ntile; ++it) {
+      const int stg = it % NST;
+      if (s_fail || !__all_sync(0xffffffffu, mbar_wait_bounded(&full[stg], (it / NST) & 1))) s_fail = 1;
+      const uint8_t* kst = smem + stg * S::kStage;
+      const uint8_t* vst = kst + S::kCodes;
+      const uint8_t* kmt = kst + 2 * S::kCodes;
+      const uint8_t* vmt = kmt + S::kMeta;
+      if (first) {
+        first = false;
+        const int hq = 4 * hg + (g >> 1);
+        const bool live = hq < a.G;
+        float xq[KS][4];
+        load_query_channels<D, KB>(vmt + S::kMeta, (size_t)(live ? hq : 0) * D, a.io_dtype, t, live, xq);
+        float qb[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) qb[i] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const float(&x)[4] = xq[ks];
+          if constexpr (AFF) qb[ks >> 1] += (x[0] + x[1]) + (x[2] + x[3]);
+          const __half2 h01 = __floats2half2_rn(x[0], x[1]);
+          const __half2 h23 = __floats2half2_rn(x[2], x[3]);
+          qf[ks][0] = h2u(h01);
+          qf[ks][1] = h2u(h23);
+          if (g & 1) {
+            const float2 f01 = __half22float2(h01);
+            const float2 f23 = __half22float2(h23);
+            qf[ks][0] = h2u(__floats2half2_rn(x[0] - f01.x, x[1] - f01.y));
+            qf[ks][1] = h2u(__floats2half2_rn(x[2] - f23.x, x[3] - f23.y));
+          }
+        }
+        if constexpr (AFF) {
+          // sums of q of head hd over each key group: quad 2 t holds that head
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], 1);
+            qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], 2);
+            qg[i] = __shfl_sync(0xffffffffu, qb[i], 8 * t);
+          }
+          if (2 * kng == NB) {
+#pragma unroll
+            for (int j = 0; j < NB / 2; ++j) qg[j] = qg[2 * j] + qg[2 * j + 1];
+          } else if (kng == 1) {
+#pragma unroll
+            for (int j = 1; j < NB; ++j) qg[0] += qg[j];
+          }
+        }
+      }
+      const bool in_pre = u.j < pre.tiles;
+      const int nv = in_pre ? pre.len - u.j * 64 : own_len - (u.j - pre.tiles) * 64;   // live rows of the tile
+      auto block = [&](auto masked) {
+        constexpr bool MASK = decltype(masked)::value;
+        float acc[NACC][4];
+#pragma unroll
+        for (int i = 0; i < NACC; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+        if constexpr (KB == 4) {
+#pragma unroll
+          for (int pb = 0; pb < NB; ++pb) {
+            __half2 h0[4], h1[4];
+            nibbles_to_h2(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * pb + 4 * t)), h0);
+            nibbles_to_h2(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * pb + 4 * t)), h1);
+            const uint32_t ka0[4] = {h2u(h0[0]), h2u(h1[0]), h2u(h0[2]), h2u(h1[2])};
+            const uint32_t ka1[4] = {h2u(h0[1]), h2u(h1[1]), h2u(h0[3]), h2u(h1[3])};
+            mma_f16(acc[pb], ka0, qf[2 * pb][0], qf[2 * pb][1]);
+            mma_f16(acc[pb], ka1, qf[2 * pb + 1][0], qf[2 * pb + 1][1]);
+          }
+        } else if constexpr (KB == 8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            __half2 l0, h0, l1, h1;
+            bytes_to_h2(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * ks + 4 * t)) ^ 0x80808080u,
+                        l0, h0);
+            bytes_to_h2(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * ks + 4 * t)) ^ 0x80808080u,
+                        l1, h1);
+            const uint32_t ka[4] = {h2u(l0), h2u(l1), h2u(h0), h2u(h1)};
+            mma_f16(acc[ks >> 1], ka, qf[ks][0], qf[ks][1]);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint2 v0 = *reinterpret_cast<const uint2*>(kst + swz_off<ROW>(rk[0], 32 * ks + 8 * t));
+            const uint2 v1 = *reinterpret_cast<const uint2*>(kst + swz_off<ROW>(rk[1], 32 * ks + 8 * t));
+            const uint32_t ka[4] = {v0.x, v1.x, v0.y, v1.y};
+            mma_f16(acc[0], ka, qf[ks][0], qf[ks][1]);
+          }
+        }
+        bool vk[2];
+        float sc[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          vk[e] = !MASK || rk[e] < nv;
+          float v = 0.0f;
+          if constexpr (AFF) {
+            // s * sum(q u) + z * sum(q) per scale group of 32, 64 or 128 channels
+            float x[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) x[nb] = acc[nb][2 * e] + acc[nb][2 * e + 1];
+            const uint8_t* mrow = kmt + rk[e] * (4 * kng);
+            if (kng == 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(mrow);
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < NB; ++j) {
+                const float2 sz = __half22float2(u2h(ws[j]));
+                v = fmaf(sz.x, x[j], fmaf(sz.y, qg[j], v));
+              }
+            } else if (kng == 2) {
+              const uint2 w = *reinterpret_cast<const uint2*>(mrow);
+              const uint32_t ws[2] = {w.x, w.y};
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float2 sz = __half22float2(u2h(ws[j]));
+                const float xj = NB == 4 ? x[2 * j] + x[2 * j + 1] : x[j];
+                v = fmaf(sz.x, xj, fmaf(sz.y, qg[j], v));
+              }
+            } else {
+              const float2 sz = __half22float2(u2h(*reinterpret_cast<const uint32_t*>(mrow)));
+              float xs = x[0];
+#pragma unroll
+              for (int j = 1; j < NB; ++j) xs += x[j];
+              v = fmaf(sz.x, xs, sz.y * qg[0]);
+            }
+          } else {
+            v = acc[0][2 * e] + acc[0][2 * e + 1];
+          }
+          sc[e] = vk[e] ? v * a.qscale : neg_inf();
+        }
+        // online softmax (log2); the block's first row is live
+        float mb = fmaxf(sc[0], sc[1]);
+        if (__any_sync(0xffffffffu, mb > m_run)) {
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 4));
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
+          const float mn = fmaxf(m_run, mb);
+          if (mn > m_run) {
+            const float alpha = fast_exp2(m_run - mn);
+            l_part *= alpha;
+            zacc *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              oacc[mt][0] *= alpha; oacc[mt][1] *= alpha; oacc[mt][2] *= alpha; oacc[mt][3] *= alpha;
+            }
+            m_run = mn;
+          }
+        }
+        float pr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          pr[e] = fast_exp2(sc[e] - m_run);
+          l_part += pr[e];
+        }
+        // Rows past the end hold whatever the page holds: weight 0, and scale and
+        // zero (or fp16 values) zeroed so that no NaN reaches the products.
+        bool vok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vok[i] = !MASK || rr[i] < nv;
+        __half2 sAB = u2h(0u), zAB = u2h(0u), sCD = u2h(0u), zCD = u2h(0u);
+        if constexpr (AFF) {
+          const uint32_t* vm = reinterpret_cast<const uint32_t*>(vmt);
+          if (vfold) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float2 sz = __half22float2(u2h(vm[rk[e]]));
+              if (!vk[e]) sz = make_float2(0.0f, 0.0f);
+              if constexpr (KB == 8) sz.y = fmaf(-1024.0f, sz.x, sz.y);   // 8-bit codes enter as 1024 + u
+              zacc = fmaf(pr[e], sz.y, zacc);
+              pr[e] *= sz.x;
+            }
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = vok[i] ? vm[rr[i] * vng + vgi] : 0u;
+            sAB = u2h(__byte_perm(w[0], w[1], 0x5410u));
+            zAB = u2h(__byte_perm(w[0], w[1], 0x7632u));
+            sCD = u2h(__byte_perm(w[2], w[3], 0x5410u));
+            zCD = u2h(__byte_perm(w[2], w[3], 0x7632u));
+          }
+        }
+        uint32_t pb[2];
+        {
+          const __half2 ph = __floats2half2_rn(pr[0], pr[1]);
+          const float2 pf = __half22float2(ph);
+          const __half2 pl = __floats2half2_rn(pr[0] - pf.x, pr[1] - pf.y);
+          pb[0] = movmatrix_t(h2u(__lows2half2(ph, pl)));
+          pb[1] = movmatrix_t(h2u(__highs2half2(ph, pl)));
+        }
+        constexpr int NWT = VTB / 4;
+        constexpr int NW = NWT > 4 ? 4 : NWT;
+#pragma unroll
+        for (int w0 = 0; w0 < NWT; w0 += NW) {
+          if (w0 > 0) asm volatile("" ::: "memory");   // the next run's loads stay behind these products
+          uint32_t A[NW], B[NW], C[NW], E[NW];
+          lds_row_words<ROW, NW>(A, vst, rr[0], g * VTB + 4 * w0);
+          lds_row_words<ROW, NW>(B, vst, rr[1], g * VTB + 4 * w0);
+          lds_row_words<ROW, NW>(C, vst, rr[2], g * VTB + 4 * w0);
+          lds_row_words<ROW, NW>(E, vst, rr[3], g * VTB + 4 * w0);
+          if constexpr (KB == 16) {
+            if (MASK) {
+#pragma unroll
+              for (int w = 0; w < NW; ++w) {
+                A[w] = vok[0] ? A[w] : 0u;
+                B[w] = vok[1] ? B[w] : 0u;
+                C[w] = vok[2] ? C[w] : 0u;
+                E[w] = vok[3] ? E[w] : 0u;
+              }
+            }
+          }
+          const int mo = w0 * (MT / NWT);
+          if (AFF && !vfold) pvt_mma<KB, NW, MT, true>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
+          else pvt_mma<KB, NW, MT, false>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
+        }
+      };
+      const bool take = blk < nv && !s_fail && !((s_bad[stg] >> (warp & 3)) & 1);   // warp-uniform
+      if (take) {
+        if (blk + 16 <= nv) block(std::false_type{});
+        else block(std::true_type{});
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stg]);
+
+      // ---- the unit's last tile here: join the warps' states, write, start over
+      const bool ends = u.j + 1 == u.tiles;
+      if (ends || it + 1 == ntile) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l_part += __shfl_xor_sync(0xffffffffu, l_part, o);
+          zacc += __shfl_xor_sync(0xffffffffu, zacc, o);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          sm_acc[warp][t][(2 * mt) * 8 + g] = (oacc[mt][0] + oacc[mt][1]) + zacc;
+          sm_acc[warp][t][(2 * mt + 1) * 8 + g] = (oacc[mt][2] + oacc[mt][3]) + zacc;
+        }
+        if (g == 0) {
+          sm_m[warp][t] = m_run;
+          sm_l[warp][t] = l_part;
+        }
+        named_sync(1, 32 * NCW);
+        const bool final = !a.joined && begun_here && ends;
+        const long long unit = (long long)u.b * p.Hkv + u.kvh;
+        // thread i of a head group: head i / 32, channels 4 (i % 32) .. + 3 (D = 128), or two
+        // (D = 64)
+        const int i = threadIdx.x & 127, h = i >> 5, head = 4 * hg + h;
+        if (head < a.G) {
+          float mm = neg_inf(), ll = 0.0f, w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mm = fmaxf(mm, sm_m[4 * hg + k][h]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = sm_l[4 * hg + k][h] == 0.0f ? 0.0f : fast_exp2(sm_m[4 * hg + k][h] - mm);
+            ll = fmaf(sm_l[4 * hg + k][h], w[k], ll);
+          }
+          constexpr int C = D / 32;
+          float o[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int d = (i & 31) * C + c;
+            o[c] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (w[k] != 0.0f) o[c] = fmaf(w[k], sm_acc[4 * hg + k][h][(d % VCH) * 8 + d / VCH], o[c]);
+          }
+          if (final) {
+            const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+            const size_t at = ((size_t)u.b * a.Hq + (size_t)u.kvh * a.G + head) * D + (i & 31) * C;
+#pragma unroll
+            for (int c = 0; c < C; ++c) store_io(a.out, at + c, a.io_dtype, o[c] * r);
+          } else {
+            float* dst = a.parts + ((size_t)(blockIdx.x + unit) * a.G + head) * (D + kPartPad);
+#pragma unroll
+            for (int c = 0; c < C; ++c) dst[(i & 31) * C + c] = o[c];
+            if ((i & 31) == 0) {
+              dst[D] = mm;
+              dst[D + 1] = ll;
+            }
+          }
+        }
+        named_sync(1, 32 * NCW);
+        m_run = neg_inf();
+        l_part = zacc = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) oacc[mt][0] = oacc[mt][1] = oacc[mt][2] = oacc[mt][3] = 0.0f;
+        first = true;
+      }
+      if (++u.j == u.tiles) {
+        u.j = 0;
+        begun_here = true;
+        if (++u.kvh == p.Hkv) {
+          u.kvh = 0;
+          if (it + 1 < ntile) {
+            do {
+              ++u.b;
+              u.tiles = sm_start[u.b + 1] - sm_start[u.b];
+            } while (u.tiles == 0);
+            own_len = part_of(a.batch.lens[u.b], a.batch.max_pages, p.page_log2, nullptr).len;
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (s_fail && threadIdx.x == 0) {
+    // a stage never arrived: say so, and wait (bounded) for the copies still in flight
+    set_pool_status(p.status, KVQ_DEV_TIMEOUT);
+    for (int s = 0; s < NST; ++s)
+      if (s_issued[s] >= 0) mbar_wait_bounded(&full[s], s_issued[s]);
+  }
+}
+
+}  // namespace kvq

@@ -435,3 +435,22 @@ def test_refusals_with_a_pool(kvq):
     with pytest.raises(ValueError, match="CUDA tensor"):
         c.decode_attn(q, t.cpu(), n)
     assert c.status() == 0
+
+
+def test_wait_that_runs_out_reports_and_recovers(kvq):
+    # a tile that never arrives: the bounded waits give up, the status says so, the next call is right
+    H, G, D, page, lens, prefix = 2, 4, 64, 16, [100, 5], 40
+    table, pre, n = tables(lens, prefix, page, seed=51)
+    c = make_pool(kvq, "aff8", H, D, page, n, seed=52)
+    q = rand((2, H * G, D), torch.Generator().manual_seed(5), torch.bfloat16)
+    args, kw = (q, dev(table), i32(lens)), dict(prefix_pages=dev(pre), prefix_len=i32([prefix]))
+    want = c.decode_attn(*args, **kw)
+    torch.cuda.synchronize()
+    kvq.kvq_test_stall_decode_tiles(True)
+    try:
+        c.decode_attn(*args, **kw)
+        assert c.status() == kvq.DEV_TIMEOUT
+    finally:
+        kvq.kvq_test_stall_decode_tiles(False)
+    c.clear_status()
+    assert torch.equal(c.decode_attn(*args, **kw), want) and c.status() == 0
