@@ -1,16 +1,18 @@
-// Launch of paged decode attention: the streaming kernel (paged_own.cuh) and
-// the merge of the states of units that span CTAs.
-#include "paged_own.cuh"
+// Launch of paged decode attention: the shared prefix (paged_prefix.cuh), the
+// streaming kernel (paged_own.cuh) and the merge of their states.
+#include "paged_prefix.cuh"
 
 namespace kvq {
 
 namespace {
 
 // Joins a unit's states with the online-softmax rule, one warp per query
-// head.  A unit that one CTA finished is left alone; one without rows gets
-// zeros.
+// head: those of the CTAs that had tiles of it and, where the prefix was
+// taken for the whole batch, those of the prefix's runs.  A unit that one CTA
+// finished is left alone; one without rows gets zeros.
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, int Hkv, int grid) {
+__global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, const PrefixArgs f, int Hkv, int grid,
+                                                          int page_log2) {
   constexpr int C = D / 32;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -26,26 +28,38 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, int H
     n = (int)(((x1 + 1) * ctas + total - 1) / total) - c0;
   }
   if (n == 1 && !a.joined) return;
+  int runs = 0;
+  if (a.joined) {
+    const Part pre = part_of(a.batch.prefix_len[0], a.batch.max_prefix_pages, page_log2, nullptr);
+    runs = prefix_runs((pre.len + 127) >> 7, f.nsplit);
+  }
   const float* own = a.parts + ((size_t)(c0 + unit) * a.G + h) * (D + kPartPad);
   const size_t stride = (size_t)a.G * (D + kPartPad);
+  const size_t run0 = (size_t)kvh * f.nsplit * f.rows + (size_t)b * a.G + h;   // + run * f.rows
   float m = neg_inf();
   for (int i = lane; i < n; i += 32) m = fmaxf(m, own[i * stride + D]);
+  for (int i = lane; i < runs; i += 32) m = fmaxf(m, f.part_ml[run0 + (size_t)i * f.rows].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float l = 0.0f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* s = own + i * stride;
-    const float li = s[D + 1];
-    const float w = li == 0.0f ? 0.0f : fast_exp2(s[D] - m);
+  auto join = [&](float mi, float li, const float* s) {
+    const float w = li == 0.0f ? 0.0f : fast_exp2(mi - m);   // l 0: no live row
     float x[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c] = s[lane * C + c];
     l = fmaf(li, w, l);
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(w, x[c], acc[c]);
+    for (int c = 0; c < C; ++c) acc[c] = li == 0.0f ? acc[c] : fmaf(w, x[c], acc[c]);
+  };
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) join(own[i * stride + D], own[i * stride + D + 1], own + i * stride);
+#pragma unroll 4
+  for (int i = 0; i < runs; ++i) {
+    const size_t at = run0 + (size_t)i * f.rows;
+    const float2 ml = f.part_ml[at];
+    join(ml.x, ml.y, f.part_o + at * D);
   }
   const float r = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t at = ((size_t)b * a.Hq + (size_t)kvh * a.G + h) * D + lane * C;
@@ -55,8 +69,65 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, int H
 
 size_t starts_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * 4 + 255) / 256 * 256; }
 
+struct Plan {
+  int shared;     // the prefix once for the batch
+  int nq;         // row tiles of 128 per CTA of the prefix kernel
+  int nsplit;     // runs per (kv head, row tiles)
+  int row_ctas;   // CTAs along the query rows
+};
+
+Plan make_plan(const PoolView& p, int n_seqs, int G, int max_prefix_pages) {
+  Plan r{};
+  const long long rows = (long long)n_seqs * G;
+  r.shared = max_prefix_pages > 0 && n_seqs > 1;
+  if (!r.shared) return r;
+  r.nq = rows > 128 ? 2 : 1;
+  r.row_ctas = (int)((rows + 128 * r.nq - 1) / (128 * r.nq));
+  const long long units = (long long)p.Hkv * r.row_ctas;
+  const long long tiles = (((long long)max_prefix_pages << p.page_log2) + 127) >> 7;
+  long long ns = p.sms / units;
+  if (ns > tiles) ns = tiles;
+  r.nsplit = ns < 1 ? 1 : (int)ns;
+  return r;
+}
+
+size_t prefix_o_bytes(const PoolView& p, const Plan& r, int rows) {
+  return r.shared ? (size_t)p.Hkv * r.nsplit * rows * p.D * sizeof(float) : 0;
+}
+size_t prefix_ml_bytes(const PoolView& p, const Plan& r, int rows) {
+  return r.shared ? ((size_t)p.Hkv * r.nsplit * rows * sizeof(float2) + 255) / 256 * 256 : 0;
+}
+
+cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, int smem, cudaStream_t st, cudaLaunchAttribute* at) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int D, int F, int NQ>
+cudaError_t launch_prefix(const PoolView& p, const PrefixArgs& f, const Plan& r, cudaStream_t st) {
+  using S = PrefixShape<D, F, NQ>;
+  auto kern = paged_prefix_kernel<D, F, NQ>;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = once_per_device(configured, [&]() {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3(r.nsplit, p.Hkv, r.row_ctas), S::kThreads, S::kSmem, st, &at);
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, p, f);
+}
+
 template <int D, int F, int HG>
-cudaError_t launch_own(const PoolView& p, OwnArgs a, int max_tiles_per_seq, cudaStream_t st) {
+cudaError_t launch_own(const PoolView& p, const OwnArgs& a, const PrefixArgs& f, int max_tiles, cudaStream_t st) {
   using S = OwnShape<D, F, HG>;
   auto kern = paged_own_kernel<D, F, HG>;
   const int base = S::kStages * S::kStage + S::kAcc + 1024;
@@ -65,67 +136,77 @@ cudaError_t launch_own(const PoolView& p, OwnArgs a, int max_tiles_per_seq, cuda
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, base + 4097 * 4);
   });
   if (e != cudaSuccess) return e;
-  const long long most = (long long)a.batch.n_seqs * p.Hkv * max_tiles_per_seq;   // tiles, at most
+  const long long most = (long long)a.batch.n_seqs * p.Hkv * max_tiles;   // tiles, at most
   long long ctas = (long long)S::kCtas * p.sms;
   if (ctas > most) ctas = most < 1 ? 1 : most;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = base + (a.batch.n_seqs + 1) * 4;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg =
+      dependent_launch(dim3((unsigned)ctas), S::kThreads, base + (a.batch.n_seqs + 1) * 4, st, &at);
   e = cudaLaunchKernelEx(&cfg, kern, p, a);
   if (e != cudaSuccess) return e;
   note_launch();
-  cfg.gridDim = dim3(a.batch.n_seqs * p.Hkv);
-  cfg.blockDim = dim3(32 * a.G);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, (const OwnArgs)a, p.Hkv, (int)ctas);
+  cfg = dependent_launch(dim3(a.batch.n_seqs * p.Hkv), 32 * a.G, 0, st, &at);
+  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, a, f, p.Hkv, (int)ctas, p.page_log2);
   note_launch();
   return e;
 }
 
 template <int D, int F>
-cudaError_t launch_heads(const PoolView& p, const OwnArgs& a, int max_tiles, cudaStream_t st) {
-  return a.G <= 4 ? launch_own<D, F, 1>(p, a, max_tiles, st) : launch_own<D, F, 2>(p, a, max_tiles, st);
+cudaError_t launch_heads(const PoolView& p, const OwnArgs& a, const PrefixArgs& f, const Plan& r, int max_tiles,
+                         cudaStream_t st) {
+  if (r.shared) {
+    const cudaError_t e = r.nq == 1 ? launch_prefix<D, F, 1>(p, f, r, st) : launch_prefix<D, F, 2>(p, f, r, st);
+    if (e != cudaSuccess) return e;
+  }
+  return a.G <= 4 ? launch_own<D, F, 1>(p, a, f, max_tiles, st) : launch_own<D, F, 2>(p, a, f, max_tiles, st);
 }
 
 template <int D>
-cudaError_t launch_format(const PoolView& p, const OwnArgs& a, int max_tiles, cudaStream_t st) {
-  if (p.k.bits == 16) return launch_heads<D, F_FP16>(p, a, max_tiles, st);
-  if (p.k.bits == 8) return launch_heads<D, F_AFF8>(p, a, max_tiles, st);
-  return launch_heads<D, F_AFF4>(p, a, max_tiles, st);
+cudaError_t launch_format(const PoolView& p, const OwnArgs& a, const PrefixArgs& f, const Plan& r, int max_tiles,
+                          cudaStream_t st) {
+  if (p.k.bits == 16) return launch_heads<D, F_FP16>(p, a, f, r, max_tiles, st);
+  if (p.k.bits == 8) return launch_heads<D, F_AFF8>(p, a, f, r, max_tiles, st);
+  return launch_heads<D, F_AFF4>(p, a, f, r, max_tiles, st);
 }
 
 }  // namespace
 
 size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_prefix_pages) {
-  (void)max_prefix_pages;
+  const int G = Hq / p.Hkv;
   const size_t states = (size_t)4 * p.sms + (size_t)n_seqs * p.Hkv;
-  return starts_bytes(n_seqs) + states * (Hq / p.Hkv) * (p.D + kPartPad) * sizeof(float);
+  const Plan r = make_plan(p, n_seqs, G, max_prefix_pages);
+  return starts_bytes(n_seqs) + prefix_ml_bytes(p, r, n_seqs * G) + prefix_o_bytes(p, r, n_seqs * G) +
+         states * G * (p.D + kPartPad) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& d, cudaStream_t st) {
+  const int G = d.Hq / p.Hkv, rows = d.batch.n_seqs * G;
+  const Plan r = make_plan(p, d.batch.n_seqs, G, d.batch.max_prefix_pages);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(d.ws);
   OwnArgs a{};
-  a.batch = d.batch;
-  a.q = d.q;
+  PrefixArgs f{};
+  a.batch = f.batch = d.batch;
+  a.q = f.q = d.q;
+  a.io_dtype = f.io_dtype = d.io_dtype;
+  a.Hq = f.Hq = d.Hq;
+  a.G = f.G = G;
+  a.qscale = f.qscale = d.qscale;
   a.out = d.out;
-  a.starts = reinterpret_cast<int*>(d.ws);
-  a.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(d.ws) + starts_bytes(d.batch.n_seqs));
-  a.io_dtype = d.io_dtype;
-  a.Hq = d.Hq;
-  a.G = d.Hq / p.Hkv;
-  a.qscale = d.qscale;
-  a.with_prefix = d.batch.max_prefix_pages > 0;
-  a.joined = 0;
+  a.starts = reinterpret_cast<int*>(ws);
+  ws += starts_bytes(d.batch.n_seqs);
+  f.part_ml = reinterpret_cast<float2*>(ws);
+  ws += prefix_ml_bytes(p, r, rows);
+  f.part_o = reinterpret_cast<float*>(ws);
+  ws += prefix_o_bytes(p, r, rows);
+  a.parts = reinterpret_cast<float*>(ws);
+  f.rows = rows;
+  f.nsplit = r.nsplit;
+  a.with_prefix = d.batch.max_prefix_pages > 0 && !r.shared;
+  a.joined = r.shared;
   a.stall_tx = test_stall_bytes();
   auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 63) >> 6); };
-  const int max_tiles = tiles(d.batch.max_pages) + tiles(d.batch.max_prefix_pages);
-  return p.D == 64 ? launch_format<64>(p, a, max_tiles, st) : launch_format<128>(p, a, max_tiles, st);
+  const int max_tiles = tiles(d.batch.max_pages) + (a.with_prefix ? tiles(d.batch.max_prefix_pages) : 0);
+  return p.D == 64 ? launch_format<64>(p, a, f, r, max_tiles, st) : launch_format<128>(p, a, f, r, max_tiles, st);
 }
 
 }  // namespace kvq
