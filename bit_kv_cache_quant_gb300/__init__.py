@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from ctypes import POINTER, Structure, byref, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 from typing import Optional
 
@@ -138,15 +139,15 @@ _proto("snapkv_select", c_int32, c_void_p, c_int64, c_int32, c_int32, c_int32, c
        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p)
 _proto("snapkv_topk", c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p)
 _proto("kvq_rope_table", c_int32, POINTER(kvq_rope_config), POINTER(c_uint64), POINTER(c_float))
-_proto("kvq_rope_qk", c_int32, POINTER(kvq_rows), POINTER(kvq_rows), c_int32, c_int32, c_int32, c_void_p,
-       POINTER(kvq_rope), c_float, c_void_p)
+# kvq_rows, kvq_rope and kvq_paged_batch arguments: byref(struct), or its bytes
+_proto("kvq_rope_qk", c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_float, c_void_p)
 _proto("kvq_paged_layout_query", c_int32, POINTER(kvq_paged_config), POINTER(kvq_paged_layout))
 _proto("kvq_paged_init", c_int32, POINTER(kvq_paged_config), c_void_p, c_size_t, c_void_p, POINTER(c_void_p))
 _proto("kvq_paged_release", None, c_void_p)
-_proto("kvq_paged_append", c_int32, c_void_p, POINTER(kvq_paged_batch), c_int32, c_void_p, POINTER(kvq_rows),
-       POINTER(kvq_rows), POINTER(kvq_rows), c_int32, POINTER(kvq_rope), c_void_p, c_float, c_void_p)
+_proto("kvq_paged_append", c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
+       c_void_p, c_void_p, c_float, c_void_p)
 _proto("kvq_paged_workspace_bytes", c_size_t, c_void_p, c_int32, c_int32, c_int32)
-_proto("kvq_paged_decode_attn", c_int32, c_void_p, POINTER(kvq_paged_batch), c_void_p, c_void_p, c_int32, c_int32,
+_proto("kvq_paged_decode_attn", c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
        c_float, c_void_p, c_size_t, c_void_p)
 _proto("kvq_paged_status", c_int32, c_void_p, POINTER(c_int32))
 _proto("kvq_paged_clear_status", c_int32, c_void_p, c_void_p)
@@ -510,26 +511,34 @@ def kvq_rope_table(cfg: kvq_rope_config):
     return list(freqs), mag.value
 
 
-def _same_device(*ts) -> torch.device:
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device per call")
+# The paged and rotary calls run once per layer of a decode step, whose kernels take a few microseconds: the
+# checks below read each tensor's properties once, and arguments go as packed bytes in the C structs' layout.
+_cur_device = torch._C._cuda_getDevice
+_cur_stream = torch._C._cuda_getCurrentRawStream
+_ROWS = struct.Struct("@PPqqqqiP")        # kvq_rows
+_BATCH = struct.Struct("@iiPPiPP")        # kvq_paged_batch
+
+
+def _device_of(first: torch.Tensor, *rest) -> int:
+    """Index of the one CUDA device all tensors (or None) are on."""
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected a CUDA tensor on {first.device}, got one on {t.device}: one device per call")
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
     return dev
 
 
-def _on(dev: torch.device, stream, fn):
-    """fn(raw stream) with `dev` current; `stream` as in the other calls (None: the device's current one)."""
-    if dev.index == torch.cuda.current_device():
-        return fn(torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
-    with torch.cuda.device(dev):
-        return fn(_stream(stream))
+def _call(dev: int, stream, fn, *args) -> None:
+    """fn(*args, raw stream) with device `dev` current; `stream` as in the other calls (None: the current one)."""
+    if dev == _cur_device():
+        status = fn(*args, _cur_stream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status:
+        _check(status)
 
 
 def _empty(shape, dtype, dev, stream):
@@ -568,37 +577,41 @@ class Rope:
         self.freqs = torch.tensor(signed, dtype=torch.int64, device=device)   # the 64 bits of each entry
         if self.freqs.is_cuda:
             torch.cuda.current_stream(self.freqs.device).synchronize()   # usable on every stream from here on
-        self.c = kvq_rope(self.freqs.data_ptr(), rot_dim, int(self.interleaved), self.attn_factor)
+        self.arg = bytes(kvq_rope(self.freqs.data_ptr(), rot_dim, int(self.interleaved), self.attn_factor))
 
 
 def _rows(name, x: torch.Tensor, out: Optional[torch.Tensor], weight: Optional[torch.Tensor], tokens: int,
-          head_dim: int, dtype) -> kvq_rows:
+          head_dim: int, dtype) -> bytes:
+    """kvq_rows of x [tokens, heads, head_dim], as packed bytes."""
     s = x.shape
     if len(s) != 3 or s[0] != tokens or s[2] != head_dim or x.dtype is not dtype:
         raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}] {dtype}, got {tuple(s)} {x.dtype}")
-    st = x.stride()
-    if st[2] != 1:
+    i0, i1, i2 = x.stride()
+    if i2 != 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
-    ost, optr, w = (0, 0), None, None
+    o0 = o1 = optr = w = 0
     if out is not None:
-        if out.shape != s or out.dtype is not dtype or out.stride(2) != 1:
+        o0, o1, o2 = out.stride()
+        if out.shape != s or out.dtype is not dtype or o2 != 1:
             raise ValueError(f"{name}_out must have {name}'s shape and dtype, its channels contiguous")
-        ost, optr = out.stride(), out.data_ptr()
-        if (ost[0] == 0 and s[0] > 1) or (ost[1] == 0 and s[1] > 1):
+        if (o0 == 0 and s[0] > 1) or (o1 == 0 and s[1] > 1):
             raise ValueError(f"{name}_out must not be an expanded tensor")
+        optr = out.data_ptr()
     if weight is not None:
         if weight.shape != (head_dim,) or weight.dtype is not dtype or not weight.is_contiguous():
             raise ValueError(f"{name}_norm must be a contiguous [{head_dim}] tensor of {name}'s dtype")
         w = weight.data_ptr()
-    return kvq_rows(x.data_ptr(), optr, st[0], st[1], ost[0], ost[1], s[1], w)
+    return _ROWS.pack(x.data_ptr(), optr, i0, i1, o0, o1, s[1], w)
 
 
-def _int32(name, t: Optional[torch.Tensor], shape) -> Optional[int]:
+def _int32(name, t: Optional[torch.Tensor], n: int, cols: Optional[int] = None) -> int:
+    """Pointer of a contiguous int32 tensor of n (or n x cols) entries; 0 for None."""
     if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)} {t.dtype}")
+        return 0
+    if (t.dtype is not torch.int32 or t.dim() != (1 if cols is None else 2) or t.size(0) != n
+            or (cols is not None and t.size(1) != cols) or not t.is_contiguous()):
+        want = (n,) if cols is None else (n, cols)
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {want}, got {tuple(t.shape)} {t.dtype}")
     return t.data_ptr()
 
 
@@ -612,17 +625,19 @@ def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Opt
     x = q if q is not None else k
     if x is None or x.dim() != 3 or x.dtype not in DTYPES:
         raise ValueError("q and k must be [T, heads, D] fp32 / bf16 / fp16 tensors")
-    dev = _same_device(q, k, positions, q_out, k_out, q_norm, k_norm, rope.freqs if rope is not None else None)
-    tokens, head_dim = x.shape[0], x.shape[2]
-    if q is not None and q_out is None:
-        q_out = _empty(q.shape, q.dtype, dev, stream)
-    if k is not None and k_out is None:
-        k_out = _empty(k.shape, k.dtype, dev, stream)
-    rq = byref(_rows("q", q, q_out, q_norm, tokens, head_dim, x.dtype)) if q is not None else None
-    rk = byref(_rows("k", k, k_out, k_norm, tokens, head_dim, x.dtype)) if k is not None else None
-    pos = _int32("positions", positions, (tokens,))
-    rp = byref(rope.c) if rope is not None else None
-    _check(_on(dev, stream, lambda st: lib.kvq_rope_qk(rq, rk, tokens, head_dim, DTYPES[x.dtype], pos, rp, eps, st)))
+    dev = _device_of(x, k, positions, q_out, k_out, q_norm, k_norm, None if rope is None else rope.freqs)
+    tokens, head_dim, dt = x.size(0), x.size(2), x.dtype
+    rq = rk = None
+    if q is not None:
+        if q_out is None:
+            q_out = _empty(q.shape, dt, dev, stream)
+        rq = _rows("q", q, q_out, q_norm, tokens, head_dim, dt)
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k.shape, dt, dev, stream)
+        rk = _rows("k", k, k_out, k_norm, tokens, head_dim, dt)
+    _call(dev, stream, lib.kvq_rope_qk, rq, rk, tokens, head_dim, DTYPES[dt], _int32("positions", positions, tokens),
+          None if rope is None else rope.arg, eps)
     return q_out, k_out
 
 
@@ -649,8 +664,8 @@ class PagedKVCache:
             raise ValueError("buf must be a contiguous uint8 CUDA tensor")
         self.buf = buf
         h = c_void_p()
-        _check(_on(buf.device, stream, lambda st: lib.kvq_paged_init(byref(self.cfg), buf.data_ptr(), buf.numel(), st,
-                                                                     byref(h))))
+        self._dev = buf.get_device()
+        _call(self._dev, stream, lambda st: lib.kvq_paged_init(byref(self.cfg), buf.data_ptr(), buf.numel(), st, byref(h)))
         self.handle = h
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
         self._ws: Optional[torch.Tensor] = None
@@ -664,16 +679,16 @@ class PagedKVCache:
             lib.kvq_paged_release(h)
             self.handle = None
 
-    def _batch(self, page_table, seq_lens, prefix_pages, prefix_len) -> kvq_paged_batch:
-        if page_table.dim() != 2 or page_table.shape[0] != seq_lens.shape[0]:
+    def _batch(self, page_table, seq_lens, prefix_pages, prefix_len) -> bytes:
+        """kvq_paged_batch, as packed bytes."""
+        if page_table.dim() != 2 or seq_lens.dim() != 1 or page_table.size(0) != seq_lens.size(0):
             raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
         B, cols = page_table.shape
         npre = 0 if prefix_pages is None else prefix_pages.numel()
         if npre and prefix_len is None:
             raise ValueError("prefix_pages needs prefix_len")
-        return kvq_paged_batch(B, cols, _int32("page_table", page_table, (B, cols)),
-                               _int32("seq_lens", seq_lens, (B,)), npre, _int32("prefix_pages", prefix_pages, (npre,)),
-                               _int32("prefix_len", prefix_len, (1,)))
+        return _BATCH.pack(B, cols, _int32("page_table", page_table, B, cols), _int32("seq_lens", seq_lens, B), npre,
+                           _int32("prefix_pages", prefix_pages, npre), _int32("prefix_len", prefix_len, 1))
 
     def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                cu_tokens: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
@@ -687,20 +702,18 @@ class PagedKVCache:
         tokens (None: one each).  k_out, v_out: where to leave the values the stored rows stand for."""
         if k.dim() != 3 or k.dtype not in DTYPES:
             raise ValueError("k and v must be [T, Hkv, D] fp32 / bf16 / fp16 tensors")
-        dev = _same_device(self.buf, k, v, page_table, seq_lens, cu_tokens, q, prefix_len, positions, q_out, k_out,
-                           v_out, q_norm, k_norm, rope.freqs if rope is not None else None)
-        tokens, dt = k.shape[0], k.dtype
-        batch = self._batch(page_table, seq_lens, None, prefix_len)
-        if q is not None and q_out is None:
-            q_out = _empty(q.shape, q.dtype, dev, stream)
-        rq = byref(_rows("q", q, q_out, q_norm, tokens, self.head_dim, dt)) if q is not None else None
-        rk = _rows("k", k, k_out, k_norm, tokens, self.head_dim, dt)
-        rv = _rows("v", v, v_out, None, tokens, self.head_dim, dt)
-        cu = _int32("cu_tokens", cu_tokens, (batch.n_seqs + 1,))
-        pos = _int32("positions", positions, (tokens,))
-        rp = byref(rope.c) if rope is not None else None
-        _check(_on(dev, stream, lambda st: lib.kvq_paged_append(self.handle, byref(batch), tokens, cu, rq, byref(rk),
-                                                                byref(rv), DTYPES[dt], rp, pos, eps, st)))
+        dev = _device_of(self.buf, k, v, page_table, seq_lens, cu_tokens, q, prefix_len, positions, q_out, k_out,
+                         v_out, q_norm, k_norm, None if rope is None else rope.freqs)
+        tokens, dt, D = k.size(0), k.dtype, self.head_dim
+        rq = None
+        if q is not None:
+            if q_out is None:
+                q_out = _empty(q.shape, dt, dev, stream)
+            rq = _rows("q", q, q_out, q_norm, tokens, D, dt)
+        _call(dev, stream, lib.kvq_paged_append, self.handle, self._batch(page_table, seq_lens, None, prefix_len), tokens,
+              _int32("cu_tokens", cu_tokens, page_table.size(0) + 1), rq, _rows("k", k, k_out, k_norm, tokens, D, dt),
+              _rows("v", v, v_out, None, tokens, D, dt), DTYPES[dt], None if rope is None else rope.arg,
+              _int32("positions", positions, tokens), eps)
         self.launches += kvq_last_launch_count()
         return q_out
 
@@ -715,7 +728,7 @@ class PagedKVCache:
         if self._ws is None or self._ws.numel() < need:
             if self._ws is not None:
                 self._old_ws.append(self._ws)   # captured graphs may still use it
-            self._ws = _empty((need,), torch.uint8, self.buf.device, stream)
+            self._ws = _empty((need,), torch.uint8, self._dev, stream)
         return self._ws
 
     def decode_attn(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -726,29 +739,30 @@ class PagedKVCache:
         s = q.shape
         if len(s) != 3 or s[2] != self.head_dim or q.dtype not in DTYPES or not q.is_contiguous():
             raise ValueError(f"q must be a contiguous [B, Hq, {self.head_dim}] tensor, got {tuple(s)} {q.dtype}")
-        dev = _same_device(self.buf, q, page_table, seq_lens, prefix_pages, prefix_len, out, workspace)
+        dev = _device_of(self.buf, q, page_table, seq_lens, prefix_pages, prefix_len, out, workspace)
         batch = self._batch(page_table, seq_lens, prefix_pages, prefix_len)
-        if s[0] != batch.n_seqs:
+        if s[0] != page_table.size(0):
             raise ValueError("q and page_table must have one row per sequence")
         if out is None:
             out = _empty(s, q.dtype, dev, stream)
         elif out.shape != s or out.dtype is not q.dtype or not out.is_contiguous():
             raise ValueError("out must have q's shape and dtype")
-        ws = workspace if workspace is not None else self._workspace(s[0], s[1], batch.max_prefix_pages, stream)
-        _check(_on(dev, stream, lambda st: lib.kvq_paged_decode_attn(
-            self.handle, byref(batch), q.data_ptr(), out.data_ptr(), s[1], DTYPES[q.dtype], softmax_scale,
-            ws.data_ptr(), ws.numel() * ws.element_size(), st)))
+        ws = workspace
+        if ws is None:
+            ws = self._workspace(s[0], s[1], 0 if prefix_pages is None else prefix_pages.numel(), stream)
+        _call(dev, stream, lib.kvq_paged_decode_attn, self.handle, batch, q.data_ptr(), out.data_ptr(), s[1],
+              DTYPES[q.dtype], softmax_scale, ws.data_ptr(), ws.nbytes)
         self.launches += kvq_last_launch_count()
         return out
 
     def status(self) -> int:
         """The pool's status word (DEV_*); synchronises."""
         st = c_int32()
-        _check(_on(self.buf.device, None, lambda _: lib.kvq_paged_status(self.handle, byref(st))))
+        _call(self._dev, None, lambda _: lib.kvq_paged_status(self.handle, byref(st)))
         return st.value
 
     def clear_status(self, stream=None) -> None:
-        _check(_on(self.buf.device, stream, lambda st: lib.kvq_paged_clear_status(self.handle, st)))
+        _call(self._dev, stream, lib.kvq_paged_clear_status, self.handle)
 
     def plane(self, name: str) -> torch.Tensor:
         """A view of plane k_codes, v_codes, k_meta or v_meta of the pool: codes fp16 [n_pages, Hkv, page_size, D]

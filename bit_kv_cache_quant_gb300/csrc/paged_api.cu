@@ -166,10 +166,14 @@ kvq_status check_batch(const kvq_paged_batch* b, bool prefix, kvq::BatchView* v)
   return KVQ_OK;
 }
 
+// SMs of the current device (asked for once per device), 0 on failure.
 int device_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

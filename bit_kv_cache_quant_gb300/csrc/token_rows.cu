@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) token_rows_kernel(const __grid
             for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
             const T* wt = static_cast<const T*>(w->weight) + lane * E;
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = x[e] * inv * In<T>::ld(wt + e);
@@ -365,6 +365,23 @@ __device__ __forceinline__ Eight<T> pack8(const float* x) {
   return e;
 }
 
+// Two fp32 operations an instruction, each rounded as its scalar form.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+
 // How the pairs of a lane's channels x[0..8) = c .. c + 7 and x[8..16) = D / 2 + c .. lie.
 enum ChunkPairing : int {
   kStraight = 0,      // no rotation
@@ -373,29 +390,44 @@ enum ChunkPairing : int {
   kQuarter = 3,       // half layout over the first D / 2 channels: x[i], i < 8, with another lane's
 };
 
-// Codes eight channels with the group's quotient (affine_code_inv), stores them
-// and leaves the values they stand for.
+// Codes eight channels by affine_code_inv's rule, stores them and leaves the
+// values they stand for.  A quotient clamped to [0, levels] plus 1.5 * 2^23
+// is rounded to the nearest integer (ties to even) in the sum's low bits; only
+// where some quotient lies within 2^-12 of a half do the exact divisions decide.
 __device__ __forceinline__ void code_eight(uint8_t* dst, int bits, float* x, float sc, float inv, float mn, float s,
                                            float z, bool live) {
   const float levels = bits == 8 ? 255.0f : 15.0f;
-  int u[8];
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23, bits 0x4B400000
+  float u[8];
+  bool near_half = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    u[i] = affine_code_inv(x[i], sc, inv, mn, levels);
-    x[i] = fmaf((float)u[i], s, z);
+    const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], mn), inv), 0.0f), levels);
+    u[i] = __fadd_rn(t, kMagic);
+    near_half |= fabsf(__fsub_rn(t, __fsub_rn(u[i], kMagic))) > 0.5f - 0x1p-12f;
   }
-  if (!live) return;
-  if (bits == 8) {
-    uint2 w;
-    w.x = (u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24)) ^ 0x80808080u;
-    w.y = (u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24)) ^ 0x80808080u;
-    *reinterpret_cast<uint2*>(dst) = w;
-  } else {
-    uint32_t w = 0;
+  if (near_half) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= (uint32_t)u[i] << (4 * i);
-    *reinterpret_cast<uint32_t*>(dst) = w;
+    for (int i = 0; i < 8; ++i) u[i] = (float)affine_code(x[i], sc, mn, levels) + kMagic;
   }
+  uint32_t w0, w1 = 0;
+  if (bits == 8) {
+    w0 = w1 = 0u - 0x4B400000u * 0x01010101u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w0 += __float_as_uint(u[i]) << (8 * i);
+      w1 += __float_as_uint(u[4 + i]) << (8 * i);
+    }
+  } else {
+    w0 = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w0 += __float_as_uint(u[i]) << (4 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(u[i] - kMagic, s, z);
+  if (!live) return;
+  if (bits == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w0 ^ 0x80808080u, w1 ^ 0x80808080u);
+  else *reinterpret_cast<uint32_t*>(dst) = w0;
 }
 
 // store_row for a lane's two runs of eight channels; l: the lane's place in its row.
@@ -447,17 +479,28 @@ __device__ __forceinline__ void store_chunks(const PoolSide& s, size_t row, int 
   }
 }
 
+// Groups a lane copies ahead.
+template <typename T> constexpr int kDepth = sizeof(T) == 4 ? 2 : 4;
+template <typename T> constexpr int kRingBytes = kRowWarps * kDepth<T> * 2 * Eight<T>::N * 32 * 16;
+
+__device__ __forceinline__ void copy16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
 // A warp takes one token and `rows_per_warp` groups of 32 / (D / 16) head rows;
 // groups never mix queries, keys and values.
 template <int D, typename T, bool PAGED>
-__global__ void __launch_bounds__(32 * kRowWarps) token_chunks_kernel(const __grid_constant__ TokenArgs a) {
+__global__ void __launch_bounds__(32 * kRowWarps, PAGED || sizeof(T) == 4 ? 3 : 4) token_chunks_kernel(const __grid_constant__ TokenArgs a) {
   constexpr int L = D / 16;     // lanes per row
   constexpr int R = 32 / L;     // rows per group
-  constexpr int U = 2;          // groups loaded before the first is used
+  constexpr int N = Eight<T>::N;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % L, rg = lane / L;
-  const long long job = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  // the warp's number from one lane, so that all that follows from it is known to be uniform
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const long long job = (long long)blockIdx.x * kRowWarps + warp;
   const int tok = (int)(job / a.slices);
   if (tok >= a.n_tokens) return;
   const int gq = (a.q.heads + R - 1) / R, gk = (a.k.heads + R - 1) / R;
@@ -490,119 +533,165 @@ __global__ void __launch_bounds__(32 * kRowWarps) token_chunks_kernel(const __gr
   }
   if (a.positions) pos = a.positions[tok];
 
-  // sines (of each pair's first channel) and cosines of the lane's eight pairs
+  // Sines (of each pair's first channel) and cosines of the lane's eight pairs.
+  // The lanes of the R rows at the same place turn by the same angles: each
+  // works out 8 / R of them and they trade.
   float cs[8], sn[8];
   int pairing = kStraight;
   if (a.rope.freqs && g0 < gq + gk) {
     const bool inter = a.rope.interleaved != 0;
     pairing = inter ? kNeighbours : (a.rope.rot == D ? kHalves : kQuarter);
+    constexpr int M = 8 / R;
+    float mc[M], ms[M];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int k = 0; k < M; ++k) {
+      const int i = rg * M + k;
       // the pair's first channel and its index
       const int c = inter ? (i < 4 ? 0 : D / 2) + 8 * l + 2 * (i & 3) : 8 * l + i;
       const int p = inter ? c >> 1 : (pairing == kQuarter && c >= D / 4 ? c - D / 4 : c);
-      cs[i] = 1.0f;
-      sn[i] = 0.0f;
+      mc[k] = 1.0f;
+      ms[k] = 0.0f;
       if (!inter || c < a.rope.rot) {
         const long long turn = (long long)((unsigned long long)(long long)pos * a.rope.freqs[p]);
         float s, co;
         sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &co);
-        cs[i] = co * a.rope.mag;
-        sn[i] = (pairing == kQuarter && c >= D / 4 ? s : -s) * a.rope.mag;   // kQuarter: the lane's own sign
+        mc[k] = co * a.rope.mag;
+        ms[k] = (pairing == kQuarter && c >= D / 4 ? s : -s) * a.rope.mag;   // kQuarter: the lane's own sign
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = __shfl_sync(0xffffffffu, mc[i % M], (i / M) * L + l);
+      sn[i] = __shfl_sync(0xffffffffu, ms[i % M], (i / M) * L + l);
     }
   }
 
-  auto view = [&](int g, int& h, int& kind) -> const RowsView& {
+  // Each lane copies its own channels ahead into its own slots of a ring, so
+  // the copies in flight cost no registers and wait for no other lane.
+  extern __shared__ __align__(16) uint4 ring[];
+  uint4* mine_ring = ring + warp * (kDepth<T> * 2 * N * 32) + lane;
+  auto row_of = [&](int g, int& kind) {   // head row of this lane in group g
     kind = g < gq ? 0 : (g < gq + gk ? 1 : 2);
-    h = (g - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * R + rg;
-    return kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    return (g - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * R + rg;
   };
-  for (int g = g0; g < g1; g += U) {
-    Eight<T> lo[U], hi[U];
+  auto fetch = [&](int g) {
+    if (g < g1) {
+      int kind;
+      const int h = row_of(g, kind);
+      const RowsView& w = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+      // a group's spare lanes repeat the last row and store nothing
+      const T* src = static_cast<const T*>(w.in) + tok * w.in_tok + min(h, w.heads - 1) * w.in_head + 8 * l;
+      uint4* dst = mine_ring + (g - g0) % kDepth<T> * (2 * N * 32);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (g + i < g1) {
-        int h, kind;
-        const RowsView& w = view(g + i, h, kind);
-        if (h >= w.heads) h = w.heads - 1;   // a group's spare lanes repeat the last row and store nothing
-        const T* p = static_cast<const T*>(w.in) + tok * w.in_tok + h * w.in_head + 8 * l;
-        lo[i].load(p);
-        hi[i].load(p + D / 2);
+      for (int i = 0; i < N; ++i) {
+        copy16(dst + i * 32, reinterpret_cast<const uint4*>(src) + i);
+        copy16(dst + (N + i) * 32, reinterpret_cast<const uint4*>(src + D / 2) + i);
       }
     }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (g + i < g1) {
-        int h, kind;
-        const RowsView& w = view(g + i, h, kind);
-        const bool mine = h < w.heads;
-        if (!mine) h = w.heads - 1;
-        float x[16];
-        unpack8<T>(lo[i], x);
-        unpack8<T>(hi[i], x + 8);
-        if (!PAGED || kind < 2) {
-          if (w.weight) {
-            float s0 = 0.0f, s1 = 0.0f;
+  for (int i = 0; i < kDepth<T>; ++i) fetch(g0 + i);
+  int last_kind = -1;
+  Eight<T> wl, wh;
+  bool normed = false;
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) {
+    int kind;
+    const int h = row_of(g, kind);
+    const RowsView& w = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    const bool mine = h < w.heads;
+    if (kind != last_kind) {
+      last_kind = kind;
+      normed = (!PAGED || kind < 2) && w.weight != nullptr;
+      if (normed) {
+        wl.load(static_cast<const T*>(w.weight) + 8 * l);
+        wh.load(static_cast<const T*>(w.weight) + D / 2 + 8 * l);
+      }
+    }
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth<T> - 1) : "memory");
+    float x[16];
+    {
+      const uint4* src = mine_ring + (g - g0) % kDepth<T> * (2 * N * 32);
+      Eight<T> lo, hi;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              s0 = fmaf(x[e], x[e], s0);
-              s1 = fmaf(x[8 + e], x[8 + e], s1);
-            }
-            s0 += s1;
+      for (int i = 0; i < N; ++i) {
+        lo.v[i] = src[i * 32];
+        hi.v[i] = src[(N + i) * 32];
+      }
+      unpack8<T>(lo, x);
+      unpack8<T>(hi, x + 8);
+    }
+    fetch(g + kDepth<T>);
+    if (normed) {
+      float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            const float inv = 1.0f / sqrtf(s0 * (1.0f / D) + a.eps);
-            Eight<T> wl, wh;
-            const T* wt = static_cast<const T*>(w.weight) + 8 * l;
-            wl.load(wt);
-            wh.load(wt + D / 2);
-            float f[16];
-            unpack8<T>(wl, f);
-            unpack8<T>(wh, f + 8);
+      for (int e = 0; e < 16; e += 2) {
+        const float2 v = make_float2(x[e], x[e + 1]);
+        sq = fma2(v, v, sq);
+      }
+      float s0 = sq.x + sq.y;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * f[e];
-          }
-          if (pairing == kHalves) {
+      for (int o = L / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+      const float inv = rsqrtf(s0 * (1.0f / D) + a.eps);
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p = x[e], q = x[8 + e];
-              x[e] = fmaf(q, sn[e], p * cs[e]);
-              x[8 + e] = fmaf(p, -sn[e], q * cs[e]);
-            }
-          } else if (pairing == kNeighbours) {
+      for (int half = 0; half < 2; ++half) {
+        float f[8];
+        unpack8<T>(half ? wh : wl, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p = x[2 * e], q = x[2 * e + 1];
-              x[2 * e] = fmaf(q, sn[e], p * cs[e]);
-              x[2 * e + 1] = fmaf(p, -sn[e], q * cs[e]);
-            }
-          } else if (pairing == kQuarter) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float o = __shfl_xor_sync(0xffffffffu, x[e], L / 2);
-              x[e] = fmaf(o, sn[e], x[e] * cs[e]);
-            }
-          }
-        }
-        if (PAGED && kind > 0)
-          store_chunks<D>(kind == 1 ? a.ks : a.vs, (size_t)(page_row < 0 ? 0 : page_row + ((long long)h << a.page_log2)),
-                          l, mine && page_row >= 0, x);
-        if (mine && (!PAGED || kind == 0 || w.out)) {
-          T* o = static_cast<T*>(w.out) + tok * w.out_tok + h * w.out_head + 8 * l;
-          pack8<T>(x).store(o);
-          pack8<T>(x + 8).store(o + D / 2);
+        for (int e = 0; e < 8; e += 2) {
+          const float2 v = mul2(mul2(make_float2(x[8 * half + e], x[8 * half + e + 1]), inv2), make_float2(f[e], f[e + 1]));
+          x[8 * half + e] = v.x;
+          x[8 * half + e + 1] = v.y;
         }
       }
+    }
+    if (!PAGED || kind < 2) {
+      if (pairing == kHalves) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 p = make_float2(x[e], x[e + 1]), q = make_float2(x[8 + e], x[9 + e]);
+          const float2 c2 = make_float2(cs[e], cs[e + 1]), s2 = make_float2(sn[e], sn[e + 1]);
+          const float2 y = fma2(q, s2, mul2(p, c2)), z = fma2(p, make_float2(-s2.x, -s2.y), mul2(q, c2));
+          x[e] = y.x;
+          x[e + 1] = y.y;
+          x[8 + e] = z.x;
+          x[9 + e] = z.y;
+        }
+      } else if (pairing == kNeighbours) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p = x[2 * e], q = x[2 * e + 1];
+          x[2 * e] = fmaf(q, sn[e], p * cs[e]);
+          x[2 * e + 1] = fmaf(p, -sn[e], q * cs[e]);
+        }
+      } else if (pairing == kQuarter) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_xor_sync(0xffffffffu, x[e], L / 2);
+          x[e] = fmaf(o, sn[e], x[e] * cs[e]);
+        }
+      }
+    }
+    if (PAGED && kind > 0)
+      store_chunks<D>(kind == 1 ? a.ks : a.vs,
+                      (size_t)(page_row < 0 ? 0 : page_row + ((long long)min(h, w.heads - 1) << a.page_log2)), l,
+                      mine && page_row >= 0, x);
+    if (mine && (!PAGED || w.out)) {
+      T* o = static_cast<T*>(w.out) + tok * w.out_tok + h * w.out_head + 8 * l;
+      pack8<T>(x).store(o);
+      pack8<T>(x + 8).store(o + D / 2);
     }
   }
 }
 
 template <typename K>
-cudaError_t launch_rows(K kernel, const TokenArgs& a, unsigned grid, cudaStream_t st) {
+cudaError_t launch_rows(K kernel, const TokenArgs& a, unsigned grid, int smem, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(32 * kRowWarps);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -617,13 +706,13 @@ template <int E, typename T>
 cudaError_t launch_typed(const TokenArgs& a, bool paged, bool chunks, unsigned grid, cudaStream_t st) {
   constexpr int D = 32 * E;
   if constexpr (E == 2 || E == 4) {
-    if (paged) return chunks ? launch_rows(token_chunks_kernel<D, T, true>, a, grid, st)
-                             : launch_rows(token_rows_kernel<E, T, true>, a, grid, st);
+    if (paged) return chunks ? launch_rows(token_chunks_kernel<D, T, true>, a, grid, kRingBytes<T>, st)
+                             : launch_rows(token_rows_kernel<E, T, true>, a, grid, 0, st);
   }
   if constexpr (E > 1) {
-    if (chunks) return launch_rows(token_chunks_kernel<D, T, false>, a, grid, st);
+    if (chunks) return launch_rows(token_chunks_kernel<D, T, false>, a, grid, kRingBytes<T>, st);
   }
-  return launch_rows(token_rows_kernel<E, T, false>, a, grid, st);
+  return launch_rows(token_rows_kernel<E, T, false>, a, grid, 0, st);
 }
 
 template <int E>

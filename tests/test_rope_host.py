@@ -277,7 +277,11 @@ def test_binding_checks_shapes(kvq):
     with pytest.raises(ValueError, match="T, heads, D"):
         kvq.rope_qk(None, None, None, None)
     r = lambda **kw: kvq._rows("q", **{**dict(x=q, out=None, weight=None, tokens=4, head_dim=128, dtype=q.dtype), **kw})
-    assert r().heads == 8 and r().in_tok_stride == 1024
+    rows = kvq.kvq_rows.from_buffer_copy(r())
+    assert rows.heads == 8 and rows.in_tok_stride == 1024 and rows.in_ == q.data_ptr()
+    assert len(kvq._BATCH.pack(1, 2, 3, 4, 5, 6, 7)) == ctypes.sizeof(kvq.kvq_paged_batch)
+    b = kvq.kvq_paged_batch.from_buffer_copy(kvq._BATCH.pack(1, 2, 3, 4, 5, 6, 7))
+    assert [getattr(b, f) for f, _ in b._fields_] == [1, 2, 3, 4, 5, 6, 7]
     for kw, msg in ((dict(tokens=5), "must be"), (dict(x=q.float()), "must be"), (dict(x=q[..., ::2], head_dim=64),
                     "contiguous"), (dict(out=q[:, :4]), "q_out"), (dict(out=q.float()), "q_out"),
                     (dict(out=q[:1].expand(4, 8, 128)), "expanded"), (dict(weight=q[0, 0, :64]), "q_norm"),
@@ -285,9 +289,9 @@ def test_binding_checks_shapes(kvq):
         with pytest.raises(ValueError, match=msg):
             r(**kw)
     with pytest.raises(ValueError, match="int32"):
-        kvq._int32("positions", torch.zeros(4, dtype=torch.int64), (4,))
+        kvq._int32("positions", torch.zeros(4, dtype=torch.int64), 4)
     with pytest.raises(ValueError, match="int32"):
-        kvq._int32("positions", torch.zeros(5, dtype=torch.int32), (4,))
+        kvq._int32("positions", torch.zeros(5, dtype=torch.int32), 4)
     with pytest.raises(ValueError, match="scaling"):
         kvq.Rope(128, scaling="dynamic", device="cpu")
     with pytest.raises(ValueError, match="factors"):
