@@ -70,6 +70,18 @@ bool kvq::encode_rows_map(CUtensorMap* m, void* base, size_t rows, int row_bytes
   return r == CUDA_SUCCESS;
 }
 
+bool kvq::encode_columns_map(CUtensorMap* m, void* base, size_t rows, int row_bytes, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint32_t estride[2] = {1, 1};
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 thread_local std::string g_err;

@@ -10,6 +10,9 @@ namespace kvq {
 // the row length; false when the driver cannot encode it (kvq_api.cu).
 bool encode_rows_map(CUtensorMap* m, void* base, size_t rows, int row_bytes, int box_rows);
 
+// The same plane 128 bytes of box_rows rows at a time, with the 128-byte swizzle.
+bool encode_columns_map(CUtensorMap* m, void* base, size_t rows, int row_bytes, int box_rows);
+
 // The test hook of kvq_test_stall_decode_tiles: bytes a CTA's first barrier expects in excess.
 unsigned test_stall_bytes();
 
@@ -44,6 +47,9 @@ struct PoolView {
   // boxes of min(page_size, 64) rows (rows of 256 bytes as [rows][2][128]).
   CUtensorMap kmap;
   CUtensorMap vmap;
+  // fp16 pools: the same planes 128 bytes of a row at a time, boxes of min(page_size, 32) rows.
+  CUtensorMap kcols;
+  CUtensorMap vcols;
   PoolSide k, v;
   int* status;
   int Hkv, D, page, page_log2, n_pages;
@@ -91,5 +97,30 @@ size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_pref
 cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& a, cudaStream_t st);
 
 __device__ __forceinline__ void set_pool_status(int* status, int code) { atomicCAS(status, 0, code); }
+
+// Two fp32 operations an instruction, each rounded as its scalar form.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
 
 }  // namespace kvq

@@ -321,7 +321,10 @@ kvq_status kvq_paged_init(const kvq_paged_config* cfg, void* dev_mem, size_t byt
   const size_t rows = (size_t)v.Hkv * v.page * v.n_pages;
   const int box = v.page < kvq::kTmaRows ? v.page : kvq::kTmaRows;
   if (!kvq::encode_rows_map(&v.kmap, v.k.codes, rows, lay.k_row_bytes, box) ||
-      !kvq::encode_rows_map(&v.vmap, v.v.codes, rows, lay.v_row_bytes, box)) {
+      !kvq::encode_rows_map(&v.vmap, v.v.codes, rows, lay.v_row_bytes, box) ||
+      (cfg->k_format == KVQ_FMT_FP16 &&
+       (!kvq::encode_columns_map(&v.kcols, v.k.codes, rows, lay.k_row_bytes, v.page < 32 ? v.page : 32) ||
+        !kvq::encode_columns_map(&v.vcols, v.v.codes, rows, lay.v_row_bytes, v.page < 32 ? v.page : 32)))) {
     delete p;
     return fail(KVQ_ERR_CUDA, "the driver could not encode the pool's tensor maps");
   }

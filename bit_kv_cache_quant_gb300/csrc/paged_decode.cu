@@ -31,36 +31,49 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, const
   int runs = 0;
   if (a.joined) {
     const Part pre = part_of(a.batch.prefix_len[0], a.batch.max_prefix_pages, page_log2, nullptr);
-    runs = prefix_runs((pre.len + 127) >> 7, f.nsplit);
+    runs = prefix_runs((pre.len + 127) >> 7, f.nsplit) * f.streams;
   }
   const float* own = a.parts + ((size_t)(c0 + unit) * a.G + h) * (D + kPartPad);
   const size_t stride = (size_t)a.G * (D + kPartPad);
-  const size_t run0 = (size_t)kvh * f.nsplit * f.rows + (size_t)b * a.G + h;   // + run * f.rows
+  const size_t run0 = (size_t)kvh * f.nsplit * f.streams * f.rows + (size_t)b * a.G + h;   // + run * f.rows
   float m = neg_inf();
   for (int i = lane; i < n; i += 32) m = fmaxf(m, own[i * stride + D]);
   for (int i = lane; i < runs; i += 32) m = fmaxf(m, f.part_ml[run0 + (size_t)i * f.rows].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // Weights first, a lane a state; then the states' rows, several in flight.
   float l = 0.0f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-  auto join = [&](float mi, float li, const float* s) {
-    const float w = li == 0.0f ? 0.0f : fast_exp2(mi - m);   // l 0: no live row
-    float x[C];
+  auto join = [&](int count, auto state, auto rows_of) {   // state(i): (max, sum); rows_of(i): the D accumulators
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      float wi = 0.0f;
+      if (i0 + lane < count) {
+        const float2 ml = state(i0 + lane);
+        if (ml.y != 0.0f) {   // sum 0: no live row
+          wi = fast_exp2(ml.x - m);
+          l = fmaf(ml.y, wi, l);
+        }
+      }
+      const int cnt = min(32, count - i0);
+#pragma unroll 8
+      for (int i = 0; i < cnt; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wi, i);
+        const float* s = rows_of(i0 + i) + lane * C;
+        float x[C];
+        if constexpr (C == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(s);
+        else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(s);
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = s[lane * C + c];
-    l = fmaf(li, w, l);
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = li == 0.0f ? acc[c] : fmaf(w, x[c], acc[c]);
+        for (int c = 0; c < C; ++c) acc[c] = w == 0.0f ? acc[c] : fmaf(w, x[c], acc[c]);
+      }
+    }
   };
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) join(own[i * stride + D], own[i * stride + D + 1], own + i * stride);
-#pragma unroll 4
-  for (int i = 0; i < runs; ++i) {
-    const size_t at = run0 + (size_t)i * f.rows;
-    const float2 ml = f.part_ml[at];
-    join(ml.x, ml.y, f.part_o + at * D);
-  }
+  join(n, [&](int i) { return make_float2(own[i * stride + D], own[i * stride + D + 1]); },
+       [&](int i) { return own + i * stride; });
+  join(runs, [&](int i) { return f.part_ml[run0 + (size_t)i * f.rows]; },
+       [&](int i) { return f.part_o + (run0 + (size_t)i * f.rows) * D; });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float r = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t at = ((size_t)b * a.Hq + (size_t)kvh * a.G + h) * D + lane * C;
 #pragma unroll
@@ -72,7 +85,8 @@ size_t starts_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * 4 + 255) / 256 
 struct Plan {
   int shared;     // the prefix once for the batch
   int nq;         // row tiles of 128 per CTA of the prefix kernel
-  int nsplit;     // runs per (kv head, row tiles)
+  int nsplit;     // CTAs per (kv head, row tiles)
+  int streams;    // states each leaves per row
   int row_ctas;   // CTAs along the query rows
 };
 
@@ -82,6 +96,7 @@ Plan make_plan(const PoolView& p, int n_seqs, int G, int max_prefix_pages) {
   r.shared = max_prefix_pages > 0 && n_seqs > 1;
   if (!r.shared) return r;
   r.nq = rows > 128 ? 2 : 1;
+  r.streams = r.nq == 2 ? 1 : 2;
   r.row_ctas = (int)((rows + 128 * r.nq - 1) / (128 * r.nq));
   const long long units = (long long)p.Hkv * r.row_ctas;
   const long long tiles = (((long long)max_prefix_pages << p.page_log2) + 127) >> 7;
@@ -92,10 +107,10 @@ Plan make_plan(const PoolView& p, int n_seqs, int G, int max_prefix_pages) {
 }
 
 size_t prefix_o_bytes(const PoolView& p, const Plan& r, int rows) {
-  return r.shared ? (size_t)p.Hkv * r.nsplit * rows * p.D * sizeof(float) : 0;
+  return r.shared ? (size_t)p.Hkv * r.nsplit * r.streams * rows * p.D * sizeof(float) : 0;
 }
 size_t prefix_ml_bytes(const PoolView& p, const Plan& r, int rows) {
-  return r.shared ? ((size_t)p.Hkv * r.nsplit * rows * sizeof(float2) + 255) / 256 * 256 : 0;
+  return r.shared ? ((size_t)p.Hkv * r.nsplit * r.streams * rows * sizeof(float2) + 255) / 256 * 256 : 0;
 }
 
 cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, int smem, cudaStream_t st, cudaLaunchAttribute* at) {
@@ -201,9 +216,10 @@ cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& d, cud
   a.parts = reinterpret_cast<float*>(ws);
   f.rows = rows;
   f.nsplit = r.nsplit;
+  f.streams = r.streams;
   a.with_prefix = d.batch.max_prefix_pages > 0 && !r.shared;
   a.joined = r.shared;
-  a.stall_tx = test_stall_bytes();
+  a.stall_tx = f.stall_tx = test_stall_bytes();
   auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 63) >> 6); };
   const int max_tiles = tiles(d.batch.max_pages) + (a.with_prefix ? tiles(d.batch.max_prefix_pages) : 0);
   return p.D == 64 ? launch_format<64>(p, a, f, r, max_tiles, st) : launch_format<128>(p, a, f, r, max_tiles, st);

@@ -117,7 +117,11 @@ __global__ void __launch_bounds__(OwnShape<D, F, HG>::kThreads, OwnShape<D, F, H
     }
     fence_mbar_init();
   }
-  grid_dependency_wait();
+  // Behind the prefix kernel this one does not wait for it: that kernel let it
+  // start only after its own wait, when all that came before was done, and the
+  // two share nothing.  The first CTA waits at its end instead, so that the
+  // merge, which waits for this grid, has both.
+  if (!a.joined) grid_dependency_wait();
   grid_launch_dependents();
 
   // ---- tiles in front of each sequence (of one kv head)
@@ -156,7 +160,10 @@ __global__ void __launch_bounds__(OwnShape<D, F, HG>::kThreads, OwnShape<D, F, H
   }
   const long long total = (long long)sm_start[n] * p.Hkv;
   const int ctas = busy_ctas(total, gridDim.x);
-  if (blockIdx.x >= ctas) return;
+  if (blockIdx.x >= ctas) {
+    if (a.joined && lead) grid_dependency_wait();
+    return;
+  }
   const long long t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
   const int ntile = (int)(t1 - t0);   // at least one
 
@@ -584,6 +591,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, HG>::kThreads, OwnShape<D, F, H
     for (int s = 0; s < NST; ++s)
       if (s_issued[s] >= 0) mbar_wait_bounded(&full[s], s_issued[s]);
   }
+  if (a.joined && lead) grid_dependency_wait();
 }
 
 }  // namespace kvq

@@ -4,16 +4,19 @@
 //
 // For a kv head the B * G query rows (G query heads a kv head) are the 128-row
 // side of tcgen05.mma.  A CTA takes one or two such row tiles and a run of
-// 128-row tiles of the prefix; runs of different CTAs are joined by the merge.
+// 128-row tiles of the prefix, as two streams: with two row tiles each stream
+// has its own queries and both take every tile, with one they share the
+// queries and take tiles in turn.  Streams of all CTAs are joined by the merge.
 //   S = Q K^T   [128 x 128], Q and K from shared memory, fp32 in tensor memory
 //   P = 2^(S c - m) as fp16, written back over S by the softmax warps
 //   O += P V    P from tensor memory, V from shared memory, fp32 in tensor memory
-// Warps 0-3 (and 4-7 for the second row tile) own the softmax, a thread a
-// row; the next four bring keys and values into shared memory in the order the
-// matrix unit wants (128-byte swizzle): fp16 pages by TMA, 8- and 4-bit pages
-// decoded to fp16 on the way (one rounding of u * s + z); one thread of the last
-// warp issues the products.  While one row tile is in its softmax the other's
-// products run.
+// Warps 0-3 and 4-7 own the streams' softmax, a thread a row; the next four
+// bring keys and the four after them values into shared
+// memory in the order the matrix unit wants (128-byte swizzle): fp16 pages by
+// TMA, 8- and 4-bit pages (and tiles with rows to leave out) by a thread a row,
+// decoded to fp16 on the way (one rounding of u * s + z); one thread of the
+// last warp issues the products.  While one stream is in its softmax the
+// other's products run.  The loading warps hand registers to the softmax warps.
 //
 // The running maximum of a row moves only when a tile exceeds it by more than
 // 2^kSlack (weights up to 2^kSlack are exact enough in fp16 and fp32), so that
@@ -33,15 +36,17 @@ constexpr float kSlack = 8.0f;
 struct PrefixArgs {
   BatchView batch;
   const void* q;
-  float* part_o;     // [Hkv][nsplit][rows][D]
-  float2* part_ml;   // [Hkv][nsplit][rows] (max, sum)
+  float* part_o;     // [Hkv][nsplit * streams][rows][D]
+  float2* part_ml;   // [Hkv][nsplit * streams][rows] (max, sum)
   int io_dtype;
   int Hq, G, rows;   // rows = n_seqs * G
-  int nsplit;        // runs per (kv head, row tiles) at most
+  int nsplit;        // CTAs per (kv head, row tiles) at most
+  int streams;       // states a CTA leaves per row: 1, or 2 where its streams share the rows
   float qscale;
+  unsigned stall_tx; // test hook, as DecodeArgs
 };
 
-// Runs a prefix of `tiles` tiles is cut into.
+// CTAs that share a prefix of `tiles` tiles.
 __device__ __forceinline__ int prefix_runs(int tiles, int nsplit) { return tiles < nsplit ? tiles : nsplit; }
 
 // ------------------------------------------------------------- tensor memory --
@@ -60,7 +65,13 @@ __device__ __forceinline__ void tc_commit(uint64_t* m) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(m))
                : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// Waits for the loads into r (and all before them); r is an operand, so that no use of it moves up past the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // 32 columns of the warp's 32 lanes.
@@ -133,9 +144,10 @@ template <int D, int F, int NQ> struct PrefixShape {
   static constexpr int kTile = 128 * D * 2;          // a 128-row fp16 tile
   static constexpr int kStages = 2;                  // of keys and of values
   static constexpr int kSmem = NQ * kTile + 2 * kStages * kTile + 1024;
-  static constexpr int kSoft = 4 * NQ;               // softmax warps
-  static constexpr int kThreads = 32 * (kSoft + 5);
-  static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;   // tensor memory: 128 S + 128 O per row tile
+  static constexpr int kSoft = 8;                    // softmax warps
+  static constexpr int kMma = kSoft + 8;             // the warp that issues the products
+  static constexpr int kThreads = 32 * (kMma + 1);
+  static constexpr uint32_t kCols = 512;             // tensor memory: 128 S + 128 O per stream
 };
 
 // Byte offset of 16-byte chunk c (of D / 8) of row r in a swizzled tile.
@@ -152,9 +164,7 @@ __device__ __forceinline__ void store_decoded(uint8_t* tile, int r, const uint32
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
     uint4 o;
-    if constexpr (KB == 16) {
-      o = make_uint4(raw[4 * c], raw[4 * c + 1], raw[4 * c + 2], raw[4 * c + 3]);
-    } else {
+    {
       // the chunk's (scale, zero): the groups of a row are 32, 64 or 128 channels
       const uint32_t m = ng == 1 ? meta[0] : (ng == D / 64 ? meta[c >> 3] : meta[c >> 2]);
       const __half2 s = u2h(__byte_perm(m, m, 0x1010u)), z = u2h(__byte_perm(m, m, 0x3232u));
@@ -172,6 +182,14 @@ __device__ __forceinline__ void store_decoded(uint8_t* tile, int r, const uint32
   }
 }
 
+// Registers a thread (of 96 at launch: 8 warps give 32 each to 8 others).
+template <int N> __device__ __forceinline__ void raise_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void lower_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 template <int D, int F, int NQ>
 __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
     paged_prefix_kernel(const __grid_constant__ PoolView p, const __grid_constant__ PrefixArgs a) {
@@ -183,8 +201,8 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
   uint8_t* sq = smem;
   uint8_t* sk = smem + NQ * S::kTile;
   uint8_t* sv = sk + NST * S::kTile;
-  __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[NQ], p_full[NQ],
-      o_full[NQ];
+  __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], p_full[2],
+      o_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_mask[4][4];   // live rows of tile j in ring slot j & 3
   __shared__ float s_scale[NQ * 128];
@@ -194,14 +212,14 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
   const int kvh = blockIdx.y, row0 = blockIdx.z * (128 * NQ);
   if (threadIdx.x == 0) {
     s_fail = 0;
-    mbar_init(&q_full, 128);
+    mbar_init(&q_full, 128 * NQ);
     for (int i = 0; i < NST; ++i) {
       mbar_init(&k_full[i], 128);
       mbar_init(&v_full[i], 128);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < NQ; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
@@ -217,7 +235,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
   if ((int)blockIdx.x >= runs) return;   // the whole CTA, before any tensor memory is held
   const int j0 = (int)((long long)tiles * blockIdx.x / runs), j1 = (int)((long long)tiles * (blockIdx.x + 1) / runs);
   const int n = j1 - j0;
-  if (warp == S::kSoft + 4) tmem_alloc(&s_tmem, S::kCols);
+  if (warp == S::kMma) tmem_alloc(&s_tmem, S::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -230,128 +248,161 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
 
   if (warp < S::kSoft) {
     // ------------------------------------------------------------- softmax
-    const int t = warp >> 2;
+    raise_registers<128>();
+    const int t = warp >> 2;                       // the stream
+    const int qt = NQ == 2 ? t : 0;                // its row tile
+    const int mine_n = NQ == 2 ? n : (n + 1 - t) >> 1;   // its tiles
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, lane number from bit 16 on
     const uint32_t ts = tmem + lanes + t * 256, to = ts + 128;
     const int r = (warp & 3) * 32 + lane;
     wait(&q_full, 0);
-    const float c = s_scale[t * 128 + r] * a.qscale;
+    const float c = s_scale[qt * 128 + r] * a.qscale;
     float m = neg_inf(), l = 0.0f;
-    for (int j = 0; j < n; ++j) {
-      wait(&s_full[t], j & 1);
+#pragma unroll 1
+    for (int k = 0; k < mine_n; ++k) {
+      const int j = NQ == 2 ? k : 2 * k + t;
+      wait(&s_full[t], k & 1);
       tc_fence_after();
       uint32_t live[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) live[i] = s_mask[j & 3][i];
-      float top = neg_inf();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t x[32];
-        tmem_ld32(x, ts + 32 * i);
-        tmem_wait_ld();
+      // Scores in quarters of 32 columns, the next one on its way while one is used; the last
+      // stays in registers for the weights, which go to columns 64 .. 127 as those are read.
+      uint32_t xa[32], xb[32];
+      float t0 = neg_inf(), t1 = neg_inf();
+      auto mask = [&](uint32_t(&x)[32], int i) {
         if (live[i] != 0xffffffffu) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((live[i] >> e) & 1)) x[e] = 0xff800000u;
         }
+      };
+      auto highest = [&](uint32_t(&x)[32], int i) {
+        mask(x, i);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
-      }
+        for (int e = 0; e < 32; e += 4) {
+          t0 = fmaxf(fmaxf(t0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+          t1 = fmaxf(fmaxf(t1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+        }
+      };
+      tmem_ld32(xa, ts);
+      tmem_wait_ld(xa);
+      tmem_ld32(xb, ts + 32);
+      highest(xa, 0);
+      tmem_wait_ld(xb);
+      tmem_ld32(xa, ts + 64);
+      highest(xb, 1);
+      tmem_wait_ld(xa);
+      tmem_ld32(xb, ts + 96);
+      highest(xa, 2);
+      tmem_wait_ld(xb);
+      highest(xb, 3);
+      float top = fmaxf(t0, t1);
       top *= c;
-      const float lift = j == 0 ? 0.0f : kSlack;
+      const float lift = k == 0 ? 0.0f : kSlack;
       if (__any_sync(0xffffffffu, top > m + lift)) {
         const bool up = top > m + lift;
         const float mn = up ? top : m;
         const float alpha = up ? fast_exp2(m - mn) : 1.0f;
-        if (j > 0) {   // (the first tile's product overwrites the accumulators)
+        if (k > 0) {   // (the first tile's product overwrites the accumulators)
           l *= alpha;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
-            uint32_t x[32];
-            tmem_ld32(x, to + 32 * i);
-            tmem_wait_ld();
+            uint32_t y[32];
+            tmem_ld32(y, to + 32 * i);
+            tmem_wait_ld(y);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-            tmem_st32(to + 32 * i, x);
+            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+            tmem_st32(to + 32 * i, y);
           }
         }
         m = mn;
       }
       const float base = m == neg_inf() ? 0.0f : m;   // no live row yet: every weight is 2^-inf
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t x[32], w[16];
-        tmem_ld32(x, ts + 32 * i);
-        tmem_wait_ld();
-        if (live[i] != 0xffffffffu) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((live[i] >> e) & 1)) x[e] = 0xff800000u;
-        }
+      float2 sum = make_float2(0.0f, 0.0f);
+      const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
+      auto weigh = [&](uint32_t(&x)[32], int i) {
+        uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(x[2 * e]), c, -base));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(x[2 * e + 1]), c, -base));
-          sum += p0 + p1;
-          w[e] = h2u(__floats2half2_rn(p0, p1));
+          float2 v = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, base2);
+          v.x = fast_exp2(v.x);
+          v.y = fast_exp2(v.y);
+          sum = add2(sum, v);
+          w[e] = h2u(__floats2half2_rn(v.x, v.y));
         }
-        tmem_st16(ts + 16 * i, w);   // over scores this thread has read
-      }
-      l += sum;
+        tmem_st16(ts + 64 + 16 * i, w);
+      };
+      tmem_ld32(xa, ts + 64);
+      weigh(xb, 3);
+      tmem_wait_ld(xa);
+      tmem_ld32(xb, ts);
+      mask(xa, 2);
+      weigh(xa, 2);
+      tmem_wait_ld(xb);
+      tmem_ld32(xa, ts + 32);
+      mask(xb, 0);
+      weigh(xb, 0);
+      tmem_wait_ld(xa);
+      mask(xa, 1);
+      weigh(xa, 1);
+      l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&p_full[t]);
     }
-    wait(&o_full[t], 0);
+    if (mine_n > 0) wait(&o_full[t], 0);
     tc_fence_after();
-    const int row = row0 + t * 128 + r;
+    const int row = row0 + qt * 128 + r;
     const bool mine = row < a.rows && !s_fail;
-    const size_t at = ((size_t)kvh * a.nsplit + blockIdx.x) * a.rows + row;
+    const int slot = NQ == 2 ? blockIdx.x : 2 * blockIdx.x + t;
+    const size_t at = ((size_t)kvh * a.nsplit * a.streams + slot) * a.rows + row;
+    if (mine) a.part_ml[at] = make_float2(m, l);
+    if (mine_n > 0) {
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t x[32];
+        tmem_ld32(x, to + 32 * i);
+        tmem_wait_ld(x);
+        if (mine) {
+          float* dst = a.part_o + at * D + 32 * i;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t x[32];
-      tmem_ld32(x, to + 32 * i);
-      tmem_wait_ld();
-      if (mine) {
-        float* dst = a.part_o + at * D + 32 * i;
+          for (int e = 0; e < 32; e += 8) {
+            // channels in order again: eight of a chunk sit as 0 4 1 5 2 6 3 7 for 4-bit values
+            uint32_t y[8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          // channels in order again: eight of a chunk sit as 0 4 1 5 2 6 3 7 for 4-bit values
-          uint32_t y[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = KB == 4 ? x[e + 2 * (k & 3) + (k >> 2)] : x[e + k];
-          reinterpret_cast<uint4*>(dst + e)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-          reinterpret_cast<uint4*>(dst + e)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int k = 0; k < 8; ++k) y[k] = KB == 4 ? x[e + 2 * (k & 3) + (k >> 2)] : x[e + k];
+            reinterpret_cast<uint4*>(dst + e)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            reinterpret_cast<uint4*>(dst + e)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          }
         }
       }
     }
-    if (mine) a.part_ml[at] = make_float2(m, l);
-  } else if (warp < S::kSoft + 4) {
+  } else if (warp < S::kMma) {
     // -------------------------------------------- queries, keys and values
-    const int r = threadIdx.x - 32 * S::kSoft;   // a thread a row
-    for (int t = 0; t < NQ; ++t) {
+    lower_registers<64>();
+    const bool keys = warp < S::kSoft + 4;
+    const int r = (threadIdx.x - 32 * S::kSoft) & 127;   // a thread a row
+    if (keys || NQ == 2) {   // the key warps lay out the first row tile, the value warps the second
+      const int t = keys ? 0 : 1;
       const int row = row0 + t * 128 + r;
-      uint4 w[D / 8];
       float big = 0.0f;
       const bool have = row < a.rows;
-      if (have) {
-        const int b = row / a.G;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) + ((size_t)b * a.Hq + (size_t)kvh * a.G + (row - b * a.G)) * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) w[i] = src[i];
-      }
+      const int b = have ? row / a.G : 0;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(a.q) + ((size_t)b * a.Hq + (size_t)kvh * a.G + (have ? row - b * a.G : 0)) * D);
       const bool bf = a.io_dtype == KVQ_DTYPE_BF16;
-      auto value = [&](int i) {   // channel i (compile-time) of the row
-        const uint4 v = w[i >> 3];
-        const uint32_t word = (i & 7) < 2 ? v.x : (i & 7) < 4 ? v.y : (i & 7) < 6 ? v.z : v.w;
-        const uint32_t h = (i & 1) ? word >> 16 : word & 0xffffu;
-        return bf ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+      auto pair = [&](uint32_t w) {
+        return bf ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : __half22float2(u2h(w));
       };
       if (have) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) big = fmaxf(big, fabsf(value(i)));
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = src[i];
+          const float2 f0 = pair(v.x), f1 = pair(v.y), f2 = pair(v.z), f3 = pair(v.w);
+          big = fmaxf(big, fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
+                                 fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)))));
+        }
       }
       // a power of two at or above the largest magnitude
       int e = 0;
@@ -359,39 +410,50 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
       e = max(min(e, 126), -126);
       const float down = __int_as_float((127 - e) << 23);
       s_scale[t * 128 + r] = __int_as_float((127 + e) << 23);
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
-        __half2 h[4];
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (have) {
+          const uint4 v = src[i];
+          float2 f[4] = {pair(v.x), pair(v.y), pair(v.z), pair(v.w)};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c0 = KB == 4 ? k : 2 * k, c1 = KB == 4 ? k + 4 : 2 * k + 1;
-          h[k] = have ? __floats2half2_rn(value(8 * i + c0) * down, value(8 * i + c1) * down) : u2h(0u);
+          for (int k = 0; k < 4; ++k) f[k] = make_float2(f[k].x * down, f[k].y * down);
+          // 4-bit keys come as channels 0 4 1 5 2 6 3 7
+          o = KB == 4 ? make_uint4(h2u(__floats2half2_rn(f[0].x, f[2].x)), h2u(__floats2half2_rn(f[0].y, f[2].y)),
+                                   h2u(__floats2half2_rn(f[1].x, f[3].x)), h2u(__floats2half2_rn(f[1].y, f[3].y)))
+                      : make_uint4(h2u(__floats2half2_rn(f[0].x, f[0].y)), h2u(__floats2half2_rn(f[1].x, f[1].y)),
+                                   h2u(__floats2half2_rn(f[2].x, f[2].y)), h2u(__floats2half2_rn(f[3].x, f[3].y)));
         }
-        *reinterpret_cast<uint4*>(sq + t * S::kTile + tile_off(r, i)) = make_uint4(h2u(h[0]), h2u(h[1]), h2u(h[2]), h2u(h[3]));
+        *reinterpret_cast<uint4*>(sq + t * S::kTile + tile_off(r, i)) = o;
       }
+      fence_async_smem();
+      mbar_arrive(&q_full);
     }
-    fence_async_smem();
-    mbar_arrive(&q_full);
 
+    const PoolSide& side = keys ? p.k : p.v;
+    const CUtensorMap* map = keys ? &p.kcols : &p.vcols;
+    uint64_t* full = keys ? k_full : v_full;
+    uint64_t* empty = keys ? k_empty : v_empty;
+    uint8_t* ring = keys ? sk : sv;
     // the page of this thread's row of tile j (-1: none)
     auto page_of = [&](int j) {
       const int tok = (j0 + j) * 128 + r;
       return j < n && tok < pre.len ? a.batch.prefix_pages[tok >> p.page_log2] : -1;
     };
-    int id = page_of(0);
-    for (int j = 0; j < n; ++j) {
-      const int next = page_of(j + 1);
+    uint32_t raw[AFF ? RAW : 1], meta[4];
+    int id = page_of(0), next = page_of(1);
+    size_t row = 0;
+    bool ok = false, tma = false;
+    auto place = [&](int j) {   // the thread's row of tile j, which warps take it by TMA
       const int tok = (j0 + j) * 128 + r;
-      const bool ok = (unsigned)id < (unsigned)p.n_pages;
-      if (!ok && tok < pre.len) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
-      const size_t row = ok ? ((((size_t)id * p.Hkv) + kvh) << p.page_log2) + (tok & (p.page - 1)) : 0;
-      const uint32_t votes = __ballot_sync(0xffffffffu, ok);
-      const int stg = j % NST;
-      const uint32_t par = ((j / NST) & 1) ^ 1;
-      uint32_t raw[RAW], meta[4];
-      // A tile of live rows of fp16 goes by TMA.  The four warps agree on it through the mask.
-      auto load = [&](const PoolSide& s) {
-        const uint4* src = reinterpret_cast<const uint4*>(s.codes + row * ROW);
+      ok = (unsigned)id < (unsigned)p.n_pages;
+      if (!ok && j < n && tok < pre.len) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
+      row = ok ? ((((size_t)id * p.Hkv) + kvh) << p.page_log2) + (tok & (p.page - 1)) : 0;
+      tma = !AFF && __all_sync(0xffffffffu, ok);   // a warp's 32 rows, each warp for itself
+    };
+    auto load = [&]() {   // 8- and 4-bit rows into registers, ahead of their stage
+      if constexpr (AFF) {
+        const uint4* src = reinterpret_cast<const uint4*>(side.codes + row * ROW);
 #pragma unroll
         for (int i = 0; i < RAW / 4; ++i) {
           const uint4 v = ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
@@ -400,30 +462,58 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
           raw[4 * i + 2] = v.z;
           raw[4 * i + 3] = v.w;
         }
-        if constexpr (AFF) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            meta[i] = ok && i < s.n_groups ? reinterpret_cast<const uint32_t*>(s.meta)[row * s.n_groups + i] : 0u;
+        for (int i = 0; i < 4; ++i)
+          meta[i] = ok && i < side.n_groups ? reinterpret_cast<const uint32_t*>(side.meta)[row * side.n_groups + i] : 0u;
+      }
+    };
+    place(0);
+    load();
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int stg = j % NST;
+      const uint32_t votes = __ballot_sync(0xffffffffu, ok);
+      if (keys && lane == 0) s_mask[j & 3][r >> 5] = votes;
+      if (j >= NST) wait(&empty[stg], ((j / NST) & 1) ^ 1);
+      uint8_t* tile = ring + stg * S::kTile;
+      if (tma) {
+        // The warp's 32 rows: one box of 32, or two of 16 rows on pages of 16, for each half.
+        const int box = min(p.page, 32);
+        fence_async_smem();
+        if (lane == 0) mbar_expect_tx(&full[stg], 32 * ROW + (j == 0 && keys && r == 0 ? a.stall_tx : 0u));
+        else mbar_arrive(&full[stg]);
+        __syncwarp();
+        if (lane % box == 0) {   // this lane's row is a box's first
+#pragma unroll
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_columns(tile + h * 16384 + r * 128, map, h * 128, (int)row, &full[stg]);
         }
-      };
-      if (lane == 0) s_mask[j & 3][r >> 5] = votes;
-      load(p.k);
-      if (j >= NST) wait(&k_empty[stg], par);
-      store_decoded<D, F>(sk + stg * S::kTile, r, raw, meta, p.k.n_groups);
-      fence_async_smem();
-      mbar_arrive(&k_full[stg]);
-      load(p.v);
-      if (j >= NST) wait(&v_empty[stg], par);
-      store_decoded<D, F>(sv + stg * S::kTile, r, raw, meta, p.v.n_groups);
-      fence_async_smem();
-      mbar_arrive(&v_full[stg]);
+      } else {
+        if constexpr (AFF) {
+          store_decoded<D, F>(tile, r, raw, meta, side.n_groups);
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(side.codes + row * ROW);
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4*>(tile + tile_off(r, c)) = ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async_smem();
+        if (a.stall_tx && j == 0 && keys && r == 0) mbar_expect_tx(&full[stg], a.stall_tx);
+        else mbar_arrive(&full[stg]);
+      }
       id = next;
+      next = page_of(j + 2);
+      place(j + 1);
+      if (j + 1 < n) load();
     }
+    // no copy is left in flight when the CTA ends, whatever else ran out
+    if (!AFF)
+      for (int j = max(n - NST, 0); j < n; ++j) mbar_wait_bounded(&full[j % NST], (j / NST) & 1);
   } else if (lane == 0) {
     // ------------------------------------------------------------ products
     constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
-    auto scores = [&](int t, int j) {
-      const uint32_t qa = smem_u32(sq + t * S::kTile), ka = smem_u32(sk + (j % NST) * S::kTile);
+    auto scores = [&](int t, int j) {   // S of stream t = its queries against keys of tile j
+      const uint32_t qa = smem_u32(sq + (NQ == 2 ? t : 0) * S::kTile), ka = smem_u32(sk + (j % NST) * S::kTile);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
@@ -431,40 +521,68 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
       }
       tc_commit(&s_full[t]);
     };
-    wait(&q_full, 0);
-    wait(&k_full[0], 0);
-    tc_fence_after();
-    for (int t = 0; t < NQ; ++t) scores(t, 0);
-    tc_commit(&k_empty[0]);
-    for (int j = 0; j < n; ++j) {
-      const int stg = j % NST;
-      for (int t = 0; t < NQ; ++t) {
-        wait(&p_full[t], j & 1);
-        if (t == 0) wait(&v_full[stg], (j / NST) & 1);
-        tc_fence_after();
-        const uint32_t va = smem_u32(sv + stg * S::kTile);
+    auto values = [&](int t, int j, bool add) {   // O of stream t += its weights times values of tile j
+      const uint32_t va = smem_u32(sv + (j % NST) * S::kTile);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + 8 * k, operand_desc(va + k * 2048, 16384, 1024), kPV,
-                    j > 0 || k > 0);
-        if (j + 1 == n) tc_commit(&o_full[t]);
-        if (t + 1 == NQ) tc_commit(&v_empty[stg]);
-        if (j + 1 < n) {
-          if (t == 0) {
-            wait(&k_full[(j + 1) % NST], ((j + 1) / NST) & 1);
-            tc_fence_after();
+      for (int k = 0; k < 8; ++k)
+        tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + 64 + 8 * k, operand_desc(va + k * 2048, 16384, 1024), kPV,
+                  add || k > 0);
+    };
+    auto keys_in = [&](int j) {
+      wait(&k_full[j % NST], (j / NST) & 1);
+      tc_fence_after();
+    };
+    wait(&q_full, 0);
+    if constexpr (NQ == 2) {
+      keys_in(0);
+      scores(0, 0);
+      scores(1, 0);
+      tc_commit(&k_empty[0]);
+      for (int j = 0; j < n; ++j) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          wait(&p_full[t], j & 1);
+          if (t == 0) wait(&v_full[j % NST], (j / NST) & 1);
+          tc_fence_after();
+          values(t, j, j > 0);
+          if (j + 1 == n) tc_commit(&o_full[t]);
+          if (t == 1) tc_commit(&v_empty[j % NST]);
+          if (j + 1 < n) {
+            if (t == 0) keys_in(j + 1);
+            scores(t, j + 1);
+            if (t == 1) tc_commit(&k_empty[(j + 1) % NST]);
           }
-          scores(t, j + 1);
-          if (t + 1 == NQ) tc_commit(&k_empty[(j + 1) % NST]);
+        }
+      }
+    } else {
+      for (int j = 0; j < 2 && j < n; ++j) {
+        keys_in(j);
+        scores(j, j);
+        tc_commit(&k_empty[j]);
+      }
+      for (int j = 0; j < n; ++j) {
+        const int t = j & 1;
+        wait(&p_full[t], (j >> 1) & 1);
+        wait(&v_full[j % NST], (j / NST) & 1);
+        tc_fence_after();
+        values(t, j, j > 1);
+        tc_commit(&v_empty[j % NST]);
+        if (j + 2 < n) {
+          keys_in(j + 2);
+          scores(t, j + 2);
+          tc_commit(&k_empty[j % NST]);
+        } else {
+          tc_commit(&o_full[t]);
         }
       }
     }
     // the last product is done before the tensor memory goes back
-    for (int t = 0; t < NQ; ++t) mbar_wait_bounded(&o_full[t], 0);
+    for (int t = 0; t < 2; ++t)
+      if (NQ == 2 || t < n) mbar_wait_bounded(&o_full[t], 0);
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == S::kSoft + 4) tmem_free(tmem, S::kCols);
+  if (warp == S::kMma) tmem_free(tmem, S::kCols);
   if (s_fail && threadIdx.x == 0) set_pool_status(p.status, KVQ_DEV_TIMEOUT);
 }
 

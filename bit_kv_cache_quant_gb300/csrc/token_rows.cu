@@ -365,23 +365,6 @@ __device__ __forceinline__ Eight<T> pack8(const float* x) {
   return e;
 }
 
-// Two fp32 operations an instruction, each rounded as its scalar form.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;\n"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-        "l"(reinterpret_cast<unsigned long long&>(c)));
-  return d;
-}
-
 // How the pairs of a lane's channels x[0..8) = c .. c + 7 and x[8..16) = D / 2 + c .. lie.
 enum ChunkPairing : int {
   kStraight = 0,      // no rotation
