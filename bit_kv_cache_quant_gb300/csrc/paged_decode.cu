@@ -1,5 +1,6 @@
 // Launch of paged decode attention: the shared prefix (paged_prefix.cuh), the
 // streaming kernel (paged_own.cuh) and the merge of their states.
+#include "paged_own.cuh"
 #include "paged_prefix.cuh"
 
 namespace kvq {
@@ -141,22 +142,23 @@ cudaError_t launch_prefix(const PoolView& p, const PrefixArgs& f, const Plan& r,
   return cudaLaunchKernelEx(&cfg, kern, p, f);
 }
 
-template <int D, int F, int HG>
+template <int D, int F>
 cudaError_t launch_own(const PoolView& p, const OwnArgs& a, const PrefixArgs& f, int max_tiles, cudaStream_t st) {
-  using S = OwnShape<D, F, HG>;
-  auto kern = paged_own_kernel<D, F, HG>;
-  const int base = S::kStages * S::kStage + S::kAcc + 1024;
+  using S = OwnShape<D, F>;
+  auto kern = paged_own_kernel<D, F>;
+  constexpr int base = S::oStart + 1024;
+  static_assert(base + (2 * kMaxSeqs + 1) * 4 + 1536 <= 227 * 1024, "shared memory per CTA");
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = once_per_device(configured, [&]() {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, base + 4097 * 4);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, base + (2 * kMaxSeqs + 1) * 4);
   });
   if (e != cudaSuccess) return e;
   const long long most = (long long)a.batch.n_seqs * p.Hkv * max_tiles;   // tiles, at most
-  long long ctas = (long long)S::kCtas * p.sms;
+  long long ctas = p.sms;
   if (ctas > most) ctas = most < 1 ? 1 : most;
   cudaLaunchAttribute at;
   cudaLaunchConfig_t cfg =
-      dependent_launch(dim3((unsigned)ctas), S::kThreads, base + (a.batch.n_seqs + 1) * 4, st, &at);
+      dependent_launch(dim3((unsigned)ctas), S::kThreads, base + (2 * a.batch.n_seqs + 1) * 4, st, &at);
   e = cudaLaunchKernelEx(&cfg, kern, p, a);
   if (e != cudaSuccess) return e;
   note_launch();
@@ -173,7 +175,7 @@ cudaError_t launch_heads(const PoolView& p, const OwnArgs& a, const PrefixArgs& 
     const cudaError_t e = r.nq == 1 ? launch_prefix<D, F, 1>(p, f, r, st) : launch_prefix<D, F, 2>(p, f, r, st);
     if (e != cudaSuccess) return e;
   }
-  return a.G <= 4 ? launch_own<D, F, 1>(p, a, f, max_tiles, st) : launch_own<D, F, 2>(p, a, f, max_tiles, st);
+  return launch_own<D, F>(p, a, f, max_tiles, st);
 }
 
 template <int D>
@@ -188,7 +190,7 @@ cudaError_t launch_format(const PoolView& p, const OwnArgs& a, const PrefixArgs&
 
 size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_prefix_pages) {
   const int G = Hq / p.Hkv;
-  const size_t states = (size_t)4 * p.sms + (size_t)n_seqs * p.Hkv;
+  const size_t states = (size_t)p.sms + (size_t)n_seqs * p.Hkv;
   const Plan r = make_plan(p, n_seqs, G, max_prefix_pages);
   return starts_bytes(n_seqs) + prefix_ml_bytes(p, r, n_seqs * G) + prefix_o_bytes(p, r, n_seqs * G) +
          states * G * (p.D + kPartPad) * sizeof(float);
@@ -220,7 +222,7 @@ cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& d, cud
   a.with_prefix = d.batch.max_prefix_pages > 0 && !r.shared;
   a.joined = r.shared;
   a.stall_tx = f.stall_tx = test_stall_bytes();
-  auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 63) >> 6); };
+  auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 127) >> 7); };
   const int max_tiles = tiles(d.batch.max_pages) + (a.with_prefix ? tiles(d.batch.max_prefix_pages) : 0);
   return p.D == 64 ? launch_format<64>(p, a, f, r, max_tiles, st) : launch_format<128>(p, a, f, r, max_tiles, st);
 }
