@@ -5,9 +5,12 @@
 
 namespace kvq {
 
-// TMA map of a code plane of `rows` rows of `row_bytes` bytes, copied 128 bytes
-// of box_rows rows at a time into shared memory with the 128-byte swizzle;
-// false when the driver cannot encode it (kvq_api.cu).
+// TMA map of a code plane of `rows` rows of `row_bytes` bytes, copied box_rows
+// rows at a time into shared memory with the 16-byte-chunk swizzle matching
+// the row length; false when the driver cannot encode it (kvq_api.cu).
+bool encode_rows_map(CUtensorMap* m, void* base, size_t rows, int row_bytes, int box_rows);
+
+// The same plane 128 bytes of box_rows rows at a time, with the 128-byte swizzle.
 bool encode_columns_map(CUtensorMap* m, void* base, size_t rows, int row_bytes, int box_rows);
 
 // The test hook of kvq_test_stall_decode_tiles: bytes a CTA's first barrier expects in excess.
@@ -40,7 +43,11 @@ struct PoolSide {
 };
 
 struct PoolView {
-  // fp16 pools: TMA descriptors of the code planes, 128 bytes of min(page_size, 32) rows at a time.
+  // TMA descriptors of the code planes as [rows, row_bytes], swizzled by the row length;
+  // boxes of min(page_size, 64) rows (rows of 256 bytes as [rows][2][128]).
+  CUtensorMap kmap;
+  CUtensorMap vmap;
+  // fp16 pools: the same planes 128 bytes of a row at a time, boxes of min(page_size, 32) rows.
   CUtensorMap kcols;
   CUtensorMap vcols;
   PoolSide k, v;
@@ -48,8 +55,6 @@ struct PoolView {
   int Hkv, D, page, page_log2, n_pages;
   int sms;
 };
-
-constexpr int kMaxSeqs = 4096;   // sequences of a call
 
 struct BatchView {
   const int* table;

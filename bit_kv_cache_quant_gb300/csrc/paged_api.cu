@@ -18,7 +18,7 @@ struct kvq_paged_s {
 
 namespace {
 
-using kvq::kMaxSeqs;
+constexpr int kMaxSeqs = 4096;
 constexpr double kTwoPi = 6.28318530717958647692528676655900577;
 
 kvq_status fail(kvq_status s, const char* fmt, ...) {
@@ -319,9 +319,12 @@ kvq_status kvq_paged_init(const kvq_paged_config* cfg, void* dev_mem, size_t byt
   v.n_pages = cfg->n_pages;
   v.sms = sms;
   const size_t rows = (size_t)v.Hkv * v.page * v.n_pages;
-  const int box = v.page < 32 ? v.page : 32;
-  if (cfg->k_format == KVQ_FMT_FP16 && (!kvq::encode_columns_map(&v.kcols, v.k.codes, rows, lay.k_row_bytes, box) ||
-                                        !kvq::encode_columns_map(&v.vcols, v.v.codes, rows, lay.v_row_bytes, box))) {
+  const int box = v.page < kvq::kTmaRows ? v.page : kvq::kTmaRows;
+  if (!kvq::encode_rows_map(&v.kmap, v.k.codes, rows, lay.k_row_bytes, box) ||
+      !kvq::encode_rows_map(&v.vmap, v.v.codes, rows, lay.v_row_bytes, box) ||
+      (cfg->k_format == KVQ_FMT_FP16 &&
+       (!kvq::encode_columns_map(&v.kcols, v.k.codes, rows, lay.k_row_bytes, v.page < 32 ? v.page : 32) ||
+        !kvq::encode_columns_map(&v.vcols, v.v.codes, rows, lay.v_row_bytes, v.page < 32 ? v.page : 32)))) {
     delete p;
     return fail(KVQ_ERR_CUDA, "the driver could not encode the pool's tensor maps");
   }
@@ -406,11 +409,11 @@ kvq_status kvq_paged_decode_attn(kvq_paged pool, const kvq_paged_batch* batch, c
   if (n_q_heads < 1 || n_q_heads % hkv)
     return fail(KVQ_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
   if (n_q_heads / hkv > 8) return fail(KVQ_ERR_UNSUPPORTED, "more than 8 query heads per kv head");
-  // rows, and the tiles of 128 rows of every (sequence, kv head), are counted in 32 bits
+  // rows, and the tiles of 64 rows of every (sequence, kv head), are counted in 32 bits
   const int64_t cols = (int64_t)batch->max_pages + batch->max_prefix_pages;
-  const int64_t tiles = (cols * pool->cfg.page_size + 127) / 128 + 1;
+  const int64_t tiles = (cols * pool->cfg.page_size + 63) / 64 + 1;
   if (cols * pool->cfg.page_size >= INT32_MAX - 128 || tiles > INT32_MAX / batch->n_seqs / hkv)
-    return fail(KVQ_ERR_UNSUPPORTED, "n_seqs * n_kv_heads * (max_pages + max_prefix_pages) * page_size / 128 must stay "
+    return fail(KVQ_ERR_UNSUPPORTED, "n_seqs * n_kv_heads * (max_pages + max_prefix_pages) * page_size / 64 must stay "
                                      "below 2^31, and a sequence's rows below 2^31 - 128");
   const size_t need = kvq::paged_workspace_bytes(pool->view, batch->n_seqs, n_q_heads, batch->max_prefix_pages);
   if (ws_bytes < need) return fail(KVQ_ERR_CAPACITY, "workspace holds %zu bytes, the call needs %zu", ws_bytes, need);

@@ -1,6 +1,5 @@
 // Launch of paged decode attention: the shared prefix (paged_prefix.cuh), the
 // streaming kernel (paged_own.cuh) and the merge of their states.
-#include "paged_own.cuh"
 #include "paged_prefix.cuh"
 
 namespace kvq {
@@ -142,23 +141,22 @@ cudaError_t launch_prefix(const PoolView& p, const PrefixArgs& f, const Plan& r,
   return cudaLaunchKernelEx(&cfg, kern, p, f);
 }
 
-template <int D, int F>
+template <int D, int F, int M>
 cudaError_t launch_own(const PoolView& p, const OwnArgs& a, const PrefixArgs& f, int max_tiles, cudaStream_t st) {
-  using S = OwnShape<D, F>;
-  auto kern = paged_own_kernel<D, F>;
-  constexpr int base = S::oStart + 1024;
-  static_assert(base + (2 * kMaxSeqs + 1) * 4 + 1536 <= 227 * 1024, "shared memory per CTA");
+  using S = OwnShape<D, F, M>;
+  auto kern = paged_own_kernel<D, F, M>;
+  const int base = S::kStages * S::kStage + S::kAcc + 1024;
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = once_per_device(configured, [&]() {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, base + (2 * kMaxSeqs + 1) * 4);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, base + 4097 * 4);
   });
   if (e != cudaSuccess) return e;
   const long long most = (long long)a.batch.n_seqs * p.Hkv * max_tiles;   // tiles, at most
-  long long ctas = p.sms;
+  long long ctas = (long long)S::kCtas * p.sms;
   if (ctas > most) ctas = most < 1 ? 1 : most;
   cudaLaunchAttribute at;
   cudaLaunchConfig_t cfg =
-      dependent_launch(dim3((unsigned)ctas), S::kThreads, base + (2 * a.batch.n_seqs + 1) * 4, st, &at);
+      dependent_launch(dim3((unsigned)ctas), S::kThreads, base + (a.batch.n_seqs + 1) * 4, st, &at);
   e = cudaLaunchKernelEx(&cfg, kern, p, a);
   if (e != cudaSuccess) return e;
   note_launch();
@@ -175,7 +173,9 @@ cudaError_t launch_heads(const PoolView& p, const OwnArgs& a, const PrefixArgs& 
     const cudaError_t e = r.nq == 1 ? launch_prefix<D, F, 1>(p, f, r, st) : launch_prefix<D, F, 2>(p, f, r, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_own<D, F>(p, a, f, max_tiles, st);
+  if (a.G <= 4) return launch_own<D, F, kPairs>(p, a, f, max_tiles, st);
+  return a.io_dtype == KVQ_DTYPE_BF16 ? launch_own<D, F, kSingles>(p, a, f, max_tiles, st)
+                                      : launch_own<D, F, kTwoTiles>(p, a, f, max_tiles, st);
 }
 
 template <int D>
@@ -190,7 +190,7 @@ cudaError_t launch_format(const PoolView& p, const OwnArgs& a, const PrefixArgs&
 
 size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_prefix_pages) {
   const int G = Hq / p.Hkv;
-  const size_t states = (size_t)p.sms + (size_t)n_seqs * p.Hkv;
+  const size_t states = (size_t)4 * p.sms + (size_t)n_seqs * p.Hkv;
   const Plan r = make_plan(p, n_seqs, G, max_prefix_pages);
   return starts_bytes(n_seqs) + prefix_ml_bytes(p, r, n_seqs * G) + prefix_o_bytes(p, r, n_seqs * G) +
          states * G * (p.D + kPartPad) * sizeof(float);
@@ -222,7 +222,7 @@ cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& d, cud
   a.with_prefix = d.batch.max_prefix_pages > 0 && !r.shared;
   a.joined = r.shared;
   a.stall_tx = f.stall_tx = test_stall_bytes();
-  auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 127) >> 7); };
+  auto tiles = [&](int pages) { return (int)((((long long)pages << p.page_log2) + 63) >> 6); };
   const int max_tiles = tiles(d.batch.max_pages) + (a.with_prefix ? tiles(d.batch.max_prefix_pages) : 0);
   return p.D == 64 ? launch_format<64>(p, a, f, r, max_tiles, st) : launch_format<128>(p, a, f, r, max_tiles, st);
 }

@@ -2,62 +2,92 @@
 // its own rows (and, where the prefix is not worth a launch of its own, the
 // prefix rows in front of them).
 //
-// Work is cut by tiles of 128 rows, not by sequences: the tiles of all units
+// Work is cut by tiles of 64 rows, not by sequences: the tiles of all units
 // (sequence, kv head) stand in one line, CTA c of n takes those from
 // c * total / n on, and a unit that spans CTAs is joined by the merge kernel
 // from one partial state per (CTA, unit).  A ragged batch thus loads every SM
 // alike, whatever its lengths.  A CTA's tile range is found from a scan of
 // the lengths, which every CTA does for itself.
 //
-// Both products are taken transposed, with the cache on the 128-row side of
-// tcgen05.mma and the up to eight query heads, as (fp16 part, residual), in
-// 16 columns:
-//   S^T [128 rows x 16] = K Q^T, one block of columns per scale group of keys
-//   O^T [D x 16] += V^T P^T, one block of columns per scale group of values
-// Stored codes enter as the integers they are (exact in fp16; u - 128 or
-// u - 8), so the rounding of scale and zero never meets the tensor core: a
-// thread per row puts the groups' scores together as s * sum(q u') + z' *
-// sum(q) in fp32, and its softmax weight enters the second product times each
-// value group's scale, again as (fp16 part, residual); the zeros' share, sum(p
-// z'), is kept apart in fp32 per head and group.  With D = 64 the second
-// product stacks rows 0-63 and 64-127 of a tile on its 128 rows against two
-// sets of columns.
+// One warp copies: lane i looks up the pages of the CTA's i-th next tile, so
+// that the table's latency is paid once per 32 tiles, and issues that tile's
+// copies, a lane a copy (codes by TMA with the swizzle of the row length, metadata
+// and the unit's query rows by bulk copies), when its stage is free.  Four
+// warps compute, 16 rows of a tile each, with the arithmetic of
+// the contiguous cache's decode (decode_tc.cuh): transposed products on
+// mma.sync m16n8k16 with 16 rows of keys or channels of values on the wide
+// side and the heads on the narrow one (Columns), keys
+// as exact integer codes with one fp32 accumulator per 32 channels.
+// A page holds whole 16-row blocks, so a block is on one page: a bad page id
+// takes its blocks out.
 //
-// Warps 0-3: softmax, a thread a row of the tile, and the joined state's way
-// out.  Warps 4-7 bring keys, warps 8-11 values: a thread a row, several tiles
-// ahead in registers, unpacked into the swizzled layout of the products (fp16
-// rows go by TMA).  One thread of warp 12 issues the products, a tile's scores
-// while the tile before is in its softmax.
-//
-// Bound by HBM for fp16 and 8-bit rows; for 4-bit rows by shared memory, where
-// each unpacked tile is written once and read once.
+// Bound by HBM: 16 to 64 query rows per tile leave the tensor pipe idle.
 #pragma once
 
-#include "paged_tc.cuh"
+#include "decode_tc.cuh"
+#include "paged.cuh"
 
 namespace kvq {
 
 constexpr int kPartPad = 4;   // partial row: D accumulators, max, sum, 2 pad
 
+// Tiles of 64 rows of a part of `len` rows behind `cols` page-table entries (its length cut to them).
+struct Part {
+  int len, tiles;
+};
+__device__ __forceinline__ Part part_of(int len, int cols, int page_log2, int* status) {
+  long long room = (long long)cols << page_log2;
+  Part p;
+  p.len = max(len, 0);
+  if (p.len > room) {
+    p.len = (int)room;
+    if (status) set_pool_status(status, KVQ_DEV_BAD_PAGE);
+  }
+  p.tiles = (p.len + 63) >> 6;
+  return p;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* m) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(m)) : "memory");
+}
+// Barrier `id` over `threads` threads of the CTA.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
 // CTAs of a grid that share `total` tiles: every one of them has some.
 __device__ __forceinline__ int busy_ctas(long long total, int grid) { return (int)(total < grid ? total : grid); }
 
-template <int D, int F> struct OwnShape {
+// How the query heads lie in the eight columns of a product.  A 16-bit query is
+// exact in fp16 (after a power of two per head); a softmax weight is not, and
+// enters as fp16 part and residual where a column pair per head is free, or
+// where the output's own fp16 rounding would not cover its error.
+enum Columns : int {
+  kPairs = 0,     // up to four heads: column 2 j the head j's fp16 part, 2 j + 1 the residual
+  kSingles = 1,   // five to eight heads, bf16 output: a column each
+  kTwoTiles = 2,  // five to eight heads, fp16 output: two tiles of pairs
+};
+
+template <int D, int F, int M> struct OwnShape {
+  static constexpr int HT = M == kTwoTiles ? 2 : 1;          // column tiles
+  static constexpr int kHeads = M == kPairs ? 4 : 8;
   static constexpr int kBits = FmtBits<F>::v;
   static constexpr int kRow = D * kBits / 8;
   static constexpr bool kAff = F != F_FP16;
-  static constexpr int kNg = kAff ? D / 32 : 1;      // scale groups of a row, at most
-  static constexpr int kHalves = D / 64;
-  static constexpr int kTile = 128 * D * 2;
-  static constexpr int kStages = 2;                  // of keys and of values
-  static constexpr int kQTile = 16 * D * 2;
-  static constexpr int kP = 128 * 16 * kNg * 2;      // a tile's weights
-  static constexpr int kMeta = 128 * 2 * kNg * 4;    // a tile's (scale, zero) pairs of keys and values
-  static constexpr int kAhead = kRow <= 64 ? 3 : 2;  // tiles in a loading thread's registers
-  static constexpr int oK = 0, oV = kStages * kTile, oP = oV + kStages * kTile, oQ = oP + 2 * kP,
-                       oMeta = oQ + 2 * kQTile, oRed = oMeta + (kAff ? 4 * kMeta : 0),
-                       oHalf = oRed + 4 * 8 * (1 + kNg) * 4, oStart = oHalf + (D == 64 ? 64 * 8 * 4 : 0);
-  static constexpr int kThreads = 13 * 32;
+  static constexpr int kNgMax = kAff ? D / 32 : 0;
+  static constexpr int kCodes = 64 * kRow;
+  static constexpr int kMeta = 64 * kNgMax * 4;
+  static constexpr int kQ = kHeads * D * 2;
+  static constexpr int kStage = (2 * kCodes + 2 * kMeta + kQ + 1023) / 1024 * 1024;
+  static constexpr int kWarps = 4;                 // computing warps
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kAcc = kWarps * kHeads * (D + 8) * 4;   // the warps' states at a unit's end
+  // CTAs per SM: as many as keep three stages each, four at most (registers; two or three with two
+  // column tiles' accumulators)
+  static constexpr int kBySmem = kStage > 24 * 1024 ? 2 : (kStage > 12 * 1024 ? 3 : 4);
+  static constexpr int kCtas = HT == 1 ? kBySmem : (D == 128 ? 2 : (kBySmem > 3 ? 3 : kBySmem));
+  static constexpr int kRaw = (225 * 1024 / kCtas - 4096 - kAcc) / kStage;
+  static constexpr int kStages = kRaw < 2 ? 2 : (kRaw > 8 ? 8 : kRaw);
 };
 
 struct OwnArgs {
@@ -74,67 +104,99 @@ struct OwnArgs {
   unsigned stall_tx; // test hook, as DecodeArgs
 };
 
-// 16-byte chunk c of a stored row as eight fp16 integers: u - 128 in order, or
-// u - 8 in the order 0 4 1 5 2 6 3 7.
-template <int KB>
-__device__ __forceinline__ uint4 integers(const uint32_t* raw, int c) {
-  __half2 h[4];
-  if constexpr (KB == 4) {
-    nibbles_to_h2<8>(raw[c], h);
-  } else {
-    const __half2 off = u2h(0x64806480u);   // 1024 + 128
-    bytes_to_h2_1024(raw[2 * c] ^ 0x80808080u, h[0], h[1]);
-    bytes_to_h2_1024(raw[2 * c + 1] ^ 0x80808080u, h[2], h[3]);
+// Four stored bytes (u - 128 as signed bytes) as exact fp16 pairs of u - 128: byte
+// b ^ 0x80 in the mantissa of 1024, less 1152.
+__device__ __forceinline__ void signed_bytes(uint32_t x, __half2& lo, __half2& hi) {
+  const __half2 off = u2h(0x64806480u);
+  bytes_to_h2_1024(x ^ 0x80808080u, lo, hi);
+  lo = __hsub2(lo, off);
+  hi = __hsub2(hi, off);
+}
+
+// O^T += V^T . P^T for one 16-row block and every column tile, as pvt_mma
+// (decode_tc.cuh): words A, B, C, E of the thread's rows 2t, 2t + 1, 2t + 8, 2t
+// + 9 feed m-tiles mo on.  Codes enter as u - kOff, with DEQ times scale plus zero.
+template <int KB, int HT, int NW, int MT, bool DEQ>
+__device__ __forceinline__ void value_products(float (&oacc)[HT][MT][4], const uint32_t (&pb)[HT][2], int mo,
+                                               const uint32_t (&A)[NW], const uint32_t (&B)[NW],
+                                               const uint32_t (&C)[NW], const uint32_t (&E)[NW], __half2 sAB,
+                                               __half2 zAB, __half2 sCD, __half2 zCD) {
+  auto both = [&](int mt, const uint32_t(&va)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __hsub2(h[i], off);
+    for (int ht = 0; ht < HT; ++ht) mma_f16(oacc[ht][mt], va, pb[ht][0], pb[ht][1]);
+  };
+#pragma unroll
+  for (int wi = 0; wi < NW; ++wi) {
+    if constexpr (KB == 16) {
+      const uint32_t va[4] = {__byte_perm(A[wi], B[wi], 0x5410u), __byte_perm(A[wi], B[wi], 0x7632u),
+                              __byte_perm(C[wi], E[wi], 0x5410u), __byte_perm(C[wi], E[wi], 0x7632u)};
+      both(mo + wi, va);
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if constexpr (KB == 4) {
+          const uint32_t sel = half ? 0x7632u : 0x5410u;
+          __half2 h0[4], h1[4];   // h0[i]: channel 8 wi + 4 half + i of rows A, B
+          nibbles_to_h2<DEQ ? 0 : 8>(__byte_perm(A[wi], B[wi], sel), h0);
+          nibbles_to_h2<DEQ ? 0 : 8>(__byte_perm(C[wi], E[wi], sel), h1);
+          if constexpr (DEQ) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h0[i] = __hfma2(h0[i], sAB, zAB);
+              h1[i] = __hfma2(h1[i], sCD, zCD);
+            }
+          }
+#pragma unroll
+          for (int pp = 0; pp < 2; ++pp) {
+            const uint32_t va[4] = {h2u(h0[2 * pp]), h2u(h0[2 * pp + 1]), h2u(h1[2 * pp]), h2u(h1[2 * pp + 1])};
+            both(mo + 4 * wi + 2 * half + pp, va);
+          }
+        } else {
+          const uint32_t sel = half ? 0x7362u : 0x5140u;   // channels 4 wi + 2 half + 0 / 1
+          __half2 l0, h0, l1, h1;
+          if constexpr (DEQ) {
+            bytes_to_h2(__byte_perm(A[wi], B[wi], sel) ^ 0x80808080u, l0, h0);
+            bytes_to_h2(__byte_perm(C[wi], E[wi], sel) ^ 0x80808080u, l1, h1);
+            l0 = __hfma2(l0, sAB, zAB); h0 = __hfma2(h0, sAB, zAB);
+            l1 = __hfma2(l1, sCD, zCD); h1 = __hfma2(h1, sCD, zCD);
+          } else {
+            signed_bytes(__byte_perm(A[wi], B[wi], sel), l0, h0);
+            signed_bytes(__byte_perm(C[wi], E[wi], sel), l1, h1);
+          }
+          const uint32_t va[4] = {h2u(l0), h2u(h0), h2u(l1), h2u(h1)};
+          both(mo + 2 * wi + half, va);
+        }
+      }
+    }
   }
-  return make_uint4(h2u(h[0]), h2u(h[1]), h2u(h[2]), h2u(h[3]));
 }
 
-// Whether `any` holds for some thread of the four softmax warps (a barrier of theirs).
-__device__ __forceinline__ bool any_of_128(bool any) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)any)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void sync_128() { asm volatile("barrier.cta.sync 1, 128;\n" ::: "memory"); }
-
-template <int D, int F>
-__global__ void __launch_bounds__(OwnShape<D, F>::kThreads, 1)
+template <int D, int F, int M>
+__global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>::kCtas)
     paged_own_kernel(const __grid_constant__ PoolView p, const __grid_constant__ OwnArgs a) {
-  using S = OwnShape<D, F>;
-  constexpr int KB = S::kBits, ROW = S::kRow, RAW = ROW / 4, NST = S::kStages, NG = S::kNg;
+  using S = OwnShape<D, F, M>;
+  constexpr int KB = S::kBits, ROW = S::kRow, NST = S::kStages, NCW = S::kWarps;
+  constexpr int KS = D / 16, NB = D / 32, MT = D / 16, VCH = D / 8, VTB = ROW / 8;
   constexpr bool AFF = S::kAff;
+  constexpr int NACC = AFF ? NB : 1;
+  constexpr int HT = S::HT, NS = M == kPairs ? 1 : 2;   // column tiles; heads whose state a thread holds
+  constexpr int kOff = KB == 4 ? 8 : (KB == 8 ? 128 : 0);   // codes enter as u - kOff, zeros as z + kOff * s
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint32_t* sm_meta = reinterpret_cast<uint32_t*>(smem + S::oMeta);   // [4][2 NG][128]
-  float* sm_red = reinterpret_cast<float*>(smem + S::oRed);           // [4 warps][8][1 + NG]
-  float* sm_half = reinterpret_cast<float*>(smem + S::oHalf);         // [64][8] (D = 64)
-  int* sm_start = reinterpret_cast<int*>(smem + S::oStart);           // [n_seqs + 1]
-  int* sm_len = sm_start + a.batch.n_seqs + 1;                        // [n_seqs]
-  __shared__ __align__(8) uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], p_full[2];
-  __shared__ uint32_t s_tmem;
-  __shared__ uint32_t s_mask[4][4];        // live rows of tile j in ring slot j & 3
-  __shared__ float s_qsum[4][8][4];        // sum of q of a head over each 32-channel block, slot unit & 3
-  __shared__ float s_qmul[4][8];           // what brings a head's scores back to scale
-  __shared__ float s_top[4][8];
-  __shared__ int s_scan[13];
+  float(*sm_acc)[S::kHeads][D + 8] = reinterpret_cast<float(*)[S::kHeads][D + 8]>(smem + NST * S::kStage);
+  int* sm_start = reinterpret_cast<int*>(smem + NST * S::kStage + S::kAcc);   // [n_seqs + 1]
+  __shared__ __align__(8) uint64_t full[NST], empty[NST];
+  __shared__ float sm_m[NCW][S::kHeads], sm_l[NCW][S::kHeads];
+  __shared__ int s_bad[NST], s_issued[NST], s_scan[NCW + 1];
   __shared__ volatile int s_fail;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     s_fail = 0;
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&k_full[i], 128);
-      mbar_init(&v_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NCW);
+      s_issued[s] = -1;
     }
     fence_mbar_init();
   }
@@ -154,11 +216,8 @@ __global__ void __launch_bounds__(OwnShape<D, F>::kThreads, 1)
     const int per = (n + S::kThreads - 1) / S::kThreads;
     const int i0 = min(threadIdx.x * per, n), i1 = min(i0 + per, n);
     int sum = 0;
-    for (int i = i0; i < i1; ++i) {
-      const Part own = part_of(a.batch.lens[i], a.batch.max_pages, p.page_log2, lead ? p.status : nullptr);
-      sm_len[i] = own.len;
-      sum += pre.tiles + own.tiles;
-    }
+    for (int i = i0; i < i1; ++i)
+      sum += pre.tiles + part_of(a.batch.lens[i], a.batch.max_pages, p.page_log2, lead ? p.status : nullptr).tiles;
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,11 +230,11 @@ __global__ void __launch_bounds__(OwnShape<D, F>::kThreads, 1)
     for (int w = 0; w < warp; ++w) at += s_scan[w];
     for (int i = i0; i < i1; ++i) {
       sm_start[i] = at;
-      at += pre.tiles + ((sm_len[i] + 127) >> 7);
+      at += pre.tiles + part_of(a.batch.lens[i], a.batch.max_pages, p.page_log2, nullptr).tiles;
     }
     if (threadIdx.x == 0) {
       int all = 0;
-      for (int w = 0; w < 13; ++w) all += s_scan[w];
+      for (int w = 0; w <= NCW; ++w) all += s_scan[w];
       sm_start[n] = all;
     }
     __syncthreads();
@@ -190,469 +249,509 @@ __global__ void __launch_bounds__(OwnShape<D, F>::kThreads, 1)
   }
   const long long t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
   const int ntile = (int)(t1 - t0);   // at least one
-  const int kng = AFF ? p.k.n_groups : 1, vng = AFF ? p.v.n_groups : 1;
-  const int scols = 16 * NG;          // columns of one tile's scores; the outputs' follow two of them
-  constexpr uint32_t kCols = 4 * 16 * NG <= 32 ? 32 : (4 * 16 * NG <= 64 ? 64 : (4 * 16 * NG <= 128 ? 128 : 256));
-  if (warp == 12) tmem_alloc(&s_tmem, kCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * scols;
 
-  // The unit of a tile, and the step to the next tile's.
+  // Sequence, kv head and tile of the unit that tile x of the line belongs to.
   struct At {
-    int b, kvh, j, tiles, len;   // len: own rows
+    int b, kvh, j, tiles;
   };
-  At u;
-  {
-    int lo = 0, hi = n;   // the last b with sm_start[b] * Hkv <= t0
+  auto locate = [&](long long x) {
+    int lo = 0, hi = n;   // the last b with sm_start[b] * Hkv <= x
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)sm_start[mid] * p.Hkv <= t0) lo = mid;
+      if ((long long)sm_start[mid] * p.Hkv <= x) lo = mid;
       else hi = mid;
     }
-    u.b = lo;
-    u.tiles = sm_start[lo + 1] - sm_start[lo];
-    u.len = sm_len[lo];
-    const int rest = (int)(t0 - (long long)sm_start[lo] * p.Hkv);
-    u.kvh = rest / u.tiles;
-    u.j = rest - u.kvh * u.tiles;
-  }
-  auto step = [&](At& v) {
-    if (++v.j < v.tiles) return;
-    v.j = 0;
-    if (++v.kvh < p.Hkv) return;
-    v.kvh = 0;
-    do {
-      ++v.b;
-      v.tiles = v.b < n ? sm_start[v.b + 1] - sm_start[v.b] : 1;   // (behind the last unit nothing is used)
-    } while (v.tiles == 0);
-    v.len = v.b < n ? sm_len[v.b] : 0;
-  };
-  // every wait is bounded; once one runs out the others return at once, the loops
-  // keep their counts and the results are marked by the status word
-  auto wait = [&](uint64_t* m, uint32_t parity) {
-    if (!s_fail && !mbar_wait_bounded(m, parity)) s_fail = 1;
+    At r;
+    r.b = lo;
+    r.tiles = sm_start[lo + 1] - sm_start[lo];
+    const int rest = (int)(x - (long long)sm_start[lo] * p.Hkv);
+    r.kvh = rest / r.tiles;
+    r.j = rest - r.kvh * r.tiles;
+    return r;
   };
 
-  if (warp < 4) {
-    // ------------------------------------------------------------- softmax
-    const int r = threadIdx.x;
-    const uint32_t lanes = (uint32_t)warp << 21;
-    // the thread's channel of the outputs: D = 64 tiles keep rows 64-127 in lanes and columns of their own
-    const int place = D == 64 ? r & 63 : r;
-    const int vgrp = AFF ? p.v.group : D;
-    const int og = (D == 64 ? (warp & 1) * 32 : warp * 32) / vgrp;   // its value group: one per warp
-    const uint32_t to = tmem_o + lanes + (D == 64 ? (warp >> 1) * 16 * vng : 0) + 16 * og;
-    float top[8], l[8], z[8][NG];
-    bool fresh = true, whole = u.j == 0;   // the unit's state is empty; its first tile was this CTA's
-    int unit = 0;
-#pragma unroll 1
-    for (int it = 0; it < ntile; ++it) {
-      const int stg = it & 1;
-      wait(&s_full[stg], (it >> 1) & 1);
-      tc_fence_after();
-      const bool live = (s_mask[it & 3][r >> 5] >> lane) & 1;
-      const uint32_t* mk = sm_meta + (it & 3) * (2 * NG * 128) + r;
-      float v[8];
+  const int kng = p.k.n_groups, vng = p.v.n_groups;
+  if (warp == NCW) {
+    // ------------------------------------------------------------- copies
+    for (int base = 0; base < ntile && !s_fail; base += 32) {
+      const bool mine = base + lane < ntile;
+      int ids[4] = {-1, -1, -1, -1}, kvh = 0, b = 0, off = 0, np = 0;
+      bool first = false;
+      if (mine) {
+        const At u = locate(t0 + base + lane);
+        b = u.b;
+        kvh = u.kvh;
+        const bool in_pre = u.j < pre.tiles;
+        const int j = in_pre ? u.j : u.j - pre.tiles;
+        const int len = in_pre ? pre.len : part_of(a.batch.lens[b], a.batch.max_pages, p.page_log2, nullptr).len;
+        const int* pages = in_pre ? a.batch.prefix_pages : a.batch.table + (size_t)b * a.batch.max_pages;
+        const int rows = min(64, len - j * 64);
+        np = p.page_log2 >= 6 ? 1 : (rows + (1 << p.page_log2) - 1) >> p.page_log2;
+        off = (j * 64) & ((1 << p.page_log2) - 1);
+        first = u.j == 0 || base + lane == 0;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) v[h] = 0.0f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (g < kng) {
-          uint32_t x[16];
-          tmem_ld16(x, tmem + lanes + stg * scols + 16 * g);
-          float2 sz = make_float2(1.0f, 0.0f);
-          if constexpr (AFF) {
-            sz = __half22float2(u2h(mk[g * 128]));
-            sz.y = fmaf(KB == 8 ? 128.0f : 8.0f, sz.x, sz.y);
-          }
-          tmem_wait_ld(x);
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const float s = __uint_as_float(x[h]) + __uint_as_float(x[8 + h]);
-            if constexpr (AFF) v[h] = fmaf(sz.x, s, fmaf(sz.y, s_qsum[unit & 3][h][g], v[h]));
-            else v[h] = s;
-          }
-        }
+        for (int i = 0; i < 4; ++i)
+          if (i < np) ids[i] = pages[((j * 64) >> p.page_log2) + i];
       }
-      bool over = fresh;
+      const int cnt = min(32, ntile - base);
+      for (int s = 0; s < cnt; ++s) {
+        const int it = base + s, stg = it % NST;
+        if (it >= NST) {
+          if (s_fail || !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[stg], ((it / NST) - 1) & 1))) {
+            s_fail = 1;
+            break;
+          }
+        }
+        // the tile's pages, a lane a copy: lane 4 i + k takes plane k of page i, lane 16 the queries
+        const int n_pg = __shfl_sync(0xffffffffu, np, s), row0 = __shfl_sync(0xffffffffu, off, s);
+        const int head = __shfl_sync(0xffffffffu, kvh, s), seq = __shfl_sync(0xffffffffu, b, s);
+        const bool begins = __shfl_sync(0xffffffffu, first, s);
+        int id = -1;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        v[h] = live ? v[h] * s_qmul[unit & 3][h] : neg_inf();
-        if (h >= a.G) v[h] = neg_inf();
-        if (!fresh) over |= v[h] > top[h] + kSlack;
+        for (int i = 0; i < 4; ++i) {
+          const int x = __shfl_sync(0xffffffffu, ids[i], s);
+          if ((lane >> 2) == i && i < n_pg) id = x;
+        }
+        const bool ok = (unsigned)id < (unsigned)p.n_pages;
+        const unsigned good = __ballot_sync(0xffffffffu, ok);          // four lanes a page
+        uint8_t* st = smem + stg * S::kStage;
+        const int rows = min(64, 1 << p.page_log2);   // of one copy
+        const uint32_t qb = begins ? (uint32_t)(a.G * D * 2) : 0u;
+        if (lane == 0) {
+          int bad = 0;
+          for (int i = 0; i < n_pg; ++i)
+            if (!((good >> (4 * i)) & 1)) bad |= ((1 << (rows >> 4)) - 1) << (i * (rows >> 4));
+          if (bad) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
+          s_bad[stg] = bad;
+          s_issued[stg] = (it / NST) & 1;
+          mbar_expect_tx(&full[stg], (uint32_t)((__popc(good) >> 2) * rows * (2 * ROW + 4 * (kng + vng))) + qb +
+                                         (it == 0 ? a.stall_tx : 0u));
+        }
+        __syncwarp();
+        fence_async_smem();   // the stage's readers are done: order the copies behind them
+        if (ok) {
+          const int i = lane >> 2, k = lane & 3;
+          const int row = (int)((((long long)id * p.Hkv + head) << p.page_log2) + row0);
+          if (k == 0) tma_rows<ROW>(st + i * rows * ROW, &p.kmap, row, &full[stg]);
+          else if (k == 1) tma_rows<ROW>(st + S::kCodes + i * rows * ROW, &p.vmap, row, &full[stg]);
+          else if (AFF && k == 2)
+            bulk_copy(st + 2 * S::kCodes + i * rows * 4 * kng, p.k.meta + (size_t)row * kng, (uint32_t)(rows * 4 * kng),
+                      &full[stg]);
+          else if (AFF)
+            bulk_copy(st + 2 * S::kCodes + S::kMeta + i * rows * 4 * vng, p.v.meta + (size_t)row * vng,
+                      (uint32_t)(rows * 4 * vng), &full[stg]);
+        }
+        if (lane == 16 && begins)
+          bulk_copy(st + 2 * S::kCodes + 2 * S::kMeta,
+                    static_cast<const uint16_t*>(a.q) + ((size_t)seq * a.Hq + (size_t)head * a.G) * D, qb, &full[stg]);
+        __syncwarp();
       }
-      if (any_of_128(over)) {
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          float w = v[h];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-          if (lane == 0) s_top[warp][h] = w;
-        }
-        sync_128();
-        float alpha[8];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          const float w = fmaxf(fmaxf(s_top[0][h], s_top[1][h]), fmaxf(s_top[2][h], s_top[3][h]));
-          const float up = fresh ? w : fmaxf(top[h], w);
-          alpha[h] = fresh || up == neg_inf() ? 1.0f : fast_exp2(top[h] - up);
-          top[h] = up;
-        }
-        if (fresh) {
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            l[h] = 0.0f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) z[h][g] = 0.0f;
-          }
-        } else {   // the accumulators, once the product before has gone into them
-          wait(&v_empty[stg ^ 1], ((it - 1) >> 1) & 1);
-          tc_fence_after();
-          uint32_t x[16];
-          tmem_ld16(x, to);
-          tmem_wait_ld(x);
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            x[h] = __float_as_uint(__uint_as_float(x[h]) * alpha[h]);
-            x[8 + h] = __float_as_uint(__uint_as_float(x[8 + h]) * alpha[h]);
-            l[h] *= alpha[h];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) z[h][g] *= alpha[h];
-          }
-          tmem_st16(to, x);
-          tmem_wait_st();
-        }
-        fresh = false;
-      }
-#pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        v[h] = fast_exp2(v[h] - (top[h] == neg_inf() ? 0.0f : top[h]));
-        l[h] += v[h];
-      }
-      // the weights' buffer is free once the product of two tiles ago has read it
-      if (it >= 2) wait(&v_empty[stg], ((it >> 1) & 1) ^ 1);
-      uint8_t* pt = smem + S::oP + stg * S::kP;
-      const int span = D == 64 ? 2 : 1;   // sets of columns
-      const int kb = (D == 64 ? r & 63 : r) >> 3, set = D == 64 ? r >> 6 : 0;
-      uint4* pw = reinterpret_cast<uint4*>(pt + kb * (span * 2 * vng * 128) + set * (2 * vng * 128) + (r & 7) * 16);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (g < vng) {
-          float2 sz = make_float2(1.0f, 0.0f);
-          if constexpr (AFF) {
-            sz = __half22float2(u2h(mk[(NG + g) * 128]));
-            sz.y = fmaf(KB == 8 ? 128.0f : 8.0f, sz.x, sz.y);
-            if (!live) sz = make_float2(0.0f, 0.0f);   // whatever a dead row's page holds
-          }
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float w0 = v[2 * k] * sz.x, w1 = v[2 * k + 1] * sz.x;
-            const __half2 h2 = __floats2half2_rn(w0, w1);
-            const float2 f = __half22float2(h2);
-            hi[k] = h2u(h2);
-            lo[k] = h2u(__floats2half2_rn(w0 - f.x, w1 - f.y));
-            if constexpr (AFF) {
-              z[2 * k][g] = fmaf(v[2 * k], sz.y, z[2 * k][g]);
-              z[2 * k + 1][g] = fmaf(v[2 * k + 1], sz.y, z[2 * k + 1][g]);
-            }
-          }
-          pw[(2 * g) * 8] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          pw[(2 * g + 1) * 8] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      mbar_arrive(&p_full[stg]);
-
-      // ---- the unit's last tile here: its state goes out
-      const bool ends = u.j + 1 == u.tiles;
-      if (ends || it + 1 == ntile) {
-        // sums over the tile rows of the maxima's weights and of the zeros' shares
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          if (h < a.G) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-#pragma unroll
-              for (int g = 0; g < NG; ++g)
-                if (AFF && g < vng) z[h][g] += __shfl_xor_sync(0xffffffffu, z[h][g], o);
-            }
-            if (lane == 0) {
-              sm_red[(warp * 8 + h) * (1 + NG)] = l[h];
-#pragma unroll
-              for (int g = 0; g < NG; ++g)
-                if (AFF && g < vng) sm_red[(warp * 8 + h) * (1 + NG) + 1 + g] = z[h][g];
-            }
-          }
-        }
-        wait(&v_empty[stg], (it >> 1) & 1);
-        tc_fence_after();
-        uint32_t x[16];
-        tmem_ld16(x, to);
-        tmem_wait_ld(x);
-        float o[8];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) o[h] = __uint_as_float(x[h]) + __uint_as_float(x[8 + h]);
-        if (D == 64 && warp >= 2) {
-#pragma unroll
-          for (int h = 0; h < 8; ++h) sm_half[place * 8 + h] = o[h];
-        }
-        sync_128();
-        if (D == 128 || warp < 2) {
-          const bool final = !a.joined && whole && ends;
-          const long long id = (long long)u.b * p.Hkv + u.kvh;
-          // 4-bit rows hold the channels of an eight as 0 4 1 5 2 6 3 7
-          const int ch = KB == 4 ? (place & ~7) + ((place & 7) >> 1) + 4 * (place & 1) : place;
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            if (h < a.G) {
-              float sum = 0.0f, zero = 0.0f;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                sum += sm_red[(w * 8 + h) * (1 + NG)];
-                if (AFF) zero += sm_red[(w * 8 + h) * (1 + NG) + 1 + og];
-              }
-              float y = o[h] + zero;
-              if (D == 64) y += sm_half[place * 8 + h];
-              if (final) {
-                store_io(a.out, ((size_t)u.b * a.Hq + (size_t)u.kvh * a.G + h) * D + ch, a.io_dtype,
-                         sum == 0.0f ? 0.0f : y / sum);
-              } else {
-                float* dst = a.parts + ((size_t)(blockIdx.x + id) * a.G + h) * (D + kPartPad);
-                dst[ch] = y;
-                if (r == 0) {
-                  dst[D] = top[h];
-                  dst[D + 1] = sum;
-                }
-              }
-            }
-          }
-        }
-        sync_128();   // before the next unit's sums
-        tc_fence_before();
-        fresh = true;
-        ++unit;
-        whole = true;
-      }
-      step(u);
     }
-  } else if (warp < 12) {
-    // -------------------------------------------------- keys and values
-    const bool keys = warp < 8;
-    const int r = threadIdx.x & 127;   // a thread a row
-    const PoolSide& side = keys ? p.k : p.v;
-    const CUtensorMap* map = keys ? &p.kcols : &p.vcols;
-    uint64_t* full = keys ? k_full : v_full;
-    uint64_t* empty = keys ? k_empty : v_empty;
-    uint8_t* ring = smem + (keys ? S::oK : S::oV);
-    constexpr int AH = S::kAhead;
-    uint32_t raw[AH][AFF ? RAW : 1], meta[AH][AFF ? 2 * NG : 1];
-    uint4 qw[AH];
-    size_t row[AH];
-    unsigned flags[AH];   // bit 0: the row is live, 1: the warp's rows go by TMA, 2: the tile begins a unit here
-    At w = u;             // the tile whose page ids are on their way
-    int ids = -1, head = 0;
-    auto look = [&](const At& v, int it) {   // page of this thread's row of v's tile, -1: none
-      if (it >= ntile) return -1;
-      const bool in_pre = v.j < pre.tiles;
-      const int tok = (in_pre ? v.j : v.j - pre.tiles) * 128 + r;
-      if (tok >= (in_pre ? pre.len : v.len)) return -1;
-      const int id = (in_pre ? a.batch.prefix_pages : a.batch.table + (size_t)v.b * a.batch.max_pages)[tok >> p.page_log2];
-      return (unsigned)id < (unsigned)p.n_pages ? id : -2;
+  } else {
+    // ---------------------------------------------------------- products
+    const int g = lane >> 2, t = lane & 3;
+    const int blk = warp * 16;
+    const int rk[2] = {blk + tau<ROW>(g), blk + tau<ROW>(g + 8)};
+    const int rr[4] = {blk + tau<ROW>(2 * t), blk + tau<ROW>(2 * t + 1), blk + tau<ROW>(2 * t + 8),
+                       blk + tau<ROW>(2 * t + 9)};
+    const int vgi = AFF ? (g * VCH) / p.v.group : 0;
+    const bool vfold = AFF && vng == 1;
+    // the states of the thread's heads: 4 s + t in pairs, 2 t + s in singles
+    float m_run[NS], l_part[NS], zacc[NS], qmul[NS];
+    float oacc[HT][MT][4];
+    auto head_of = [&](int s) { return M == kSingles ? 2 * t + s : 4 * s + t; };
+    auto clear = [&]() {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        m_run[s] = neg_inf();
+        l_part[s] = zacc[s] = 0.0f;
+      }
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) oacc[ht][mt][0] = oacc[ht][mt][1] = oacc[ht][mt][2] = oacc[ht][mt][3] = 0.0f;
     };
-    auto fetch = [&](int s) {   // tile `head` into slot s; the ids of the next one
-      const bool ok = ids >= 0;
-      if (ids == -2) set_pool_status(p.status, KVQ_DEV_BAD_PAGE);
-      row[s] = ok ? ((((size_t)ids * p.Hkv) + w.kvh) << p.page_log2) + (r & (p.page - 1)) : 0;
-      const bool first = head < ntile && (w.j == 0 || head == 0);
-      flags[s] = (ok ? 1u : 0u) | (!AFF && __all_sync(0xffffffffu, ok) ? 2u : 0u) | (first ? 4u : 0u);
-      if constexpr (AFF) {
-        const uint4* src = reinterpret_cast<const uint4*>(side.codes + row[s] * ROW);
+    clear();
+    uint32_t qf[HT][KS][2];
+    float qg[NS][NB];
+    At u = locate(t0);
+    bool first = true, begun_here = u.j == 0;
+    int own_len = part_of(a.batch.lens[u.b], a.batch.max_pages, p.page_log2, nullptr).len;
+
+    for (int it = 0; it < ntile; ++it) {
+      const int stg = it % NST;
+      if (s_fail || !__all_sync(0xffffffffu, mbar_wait_bounded(&full[stg], (it / NST) & 1))) s_fail = 1;
+      const uint8_t* kst = smem + stg * S::kStage;
+      const uint8_t* vst = kst + S::kCodes;
+      const uint8_t* kmt = kst + 2 * S::kCodes;
+      const uint8_t* vmt = kmt + S::kMeta;
+      if (first) {
+        first = false;
 #pragma unroll
-        for (int i = 0; i < RAW / 4; ++i) {
-          const uint4 x = ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-          raw[s][4 * i] = x.x;
-          raw[s][4 * i + 1] = x.y;
-          raw[s][4 * i + 2] = x.z;
-          raw[s][4 * i + 3] = x.w;
-        }
-        if (keys) {   // the key warps bring both sides' (scale, zero) for the softmax
+        for (int ht = 0; ht < HT; ++ht) {
+          const int hq = M == kSingles ? g : 4 * ht + (g >> 1);   // the head of column g
+          const bool live = hq < a.G;
+          float xq[KS][4];
+          load_query_channels<D, KB>(vmt + S::kMeta, (size_t)(live ? hq : 0) * D, a.io_dtype, t, live, xq);
+          // a power of two brings the head's largest magnitude under one (bf16's range in fp16)
+          float big = 0.0f;
 #pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            meta[s][i] = ok && i < kng ? reinterpret_cast<const uint32_t*>(p.k.meta)[row[s] * kng + i] : 0u;
-            meta[s][NG + i] = ok && i < vng ? reinterpret_cast<const uint32_t*>(p.v.meta)[row[s] * vng + i] : 0u;
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(xq[ks][i]));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          int ex = 0;
+          if (big > 0.0f && big < __int_as_float(0x7f800000)) frexpf(big, &ex);
+          ex = max(min(ex, 126), -126);
+          const float down = __int_as_float((127 - ex) << 23);
+          const float mul = __int_as_float((127 + ex) << 23) * a.qscale;
+          float qb[NB];
+#pragma unroll
+          for (int i = 0; i < NB; ++i) qb[i] = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = xq[ks][i] * down;
+            if constexpr (AFF) qb[ks >> 1] += (x[0] + x[1]) + (x[2] + x[3]);
+            // (exact: an odd column of a pair, the queries' residual, is zero)
+            const bool zero = M != kSingles && (g & 1);
+            qf[ht][ks][0] = zero ? 0u : h2u(__floats2half2_rn(x[0], x[1]));
+            qf[ht][ks][1] = zero ? 0u : h2u(__floats2half2_rn(x[2], x[3]));
+          }
+          if constexpr (AFF) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], 1);
+              qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], 2);
+            }
+          }
+          // for the thread's own heads: the sums of q over each key group, and what brings scores back to scale
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            if (M != kTwoTiles || s == ht) {
+              const int from = M == kSingles ? 8 * t + 4 * s : 8 * t;
+              qmul[s] = __shfl_sync(0xffffffffu, mul, from);
+              if constexpr (AFF) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) qg[s][i] = __shfl_sync(0xffffffffu, qb[i], from);
+                if (2 * kng == NB) {
+#pragma unroll
+                  for (int j = 0; j < NB / 2; ++j) qg[s][j] = qg[s][2 * j] + qg[s][2 * j + 1];
+                } else if (kng == 1) {
+#pragma unroll
+                  for (int j = 1; j < NB; ++j) qg[s][0] += qg[s][j];
+                }
+              }
+            }
           }
         }
       }
-      if (keys && first && r < D && r / (D / 8) < a.G)   // eight channels of one head's query
-        qw[s] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                               ((size_t)w.b * a.Hq + (size_t)w.kvh * a.G) * D)[r];
-      else
-        qw[s] = make_uint4(0u, 0u, 0u, 0u);
-      ++head;
-      step(w);
-      ids = look(w, head);
-    };
-    ids = look(w, 0);
+      const bool in_pre = u.j < pre.tiles;
+      const int nv = in_pre ? pre.len - u.j * 64 : own_len - (u.j - pre.tiles) * 64;   // live rows of the tile
+      auto block = [&](auto masked) {
+        constexpr bool MASK = decltype(masked)::value;
+        float acc[HT][NACC][4];
 #pragma unroll
-    for (int s = 0; s < AH; ++s) fetch(s);
-    int unit = -1;
-#pragma unroll 1
-    for (int base = 0; base < ntile; base += AH) {
+        for (int ht = 0; ht < HT; ++ht)
 #pragma unroll
-      for (int s = 0; s < AH; ++s) {
-        const int it = base + s;
-        if (it < ntile) {
-          const int stg = it % NST;
-          if (it >= NST) wait(&empty[stg], ((it / NST) & 1) ^ 1);
-          uint8_t* tile = ring + stg * S::kTile;
-          if (keys) {
-            const uint32_t votes = __ballot_sync(0xffffffffu, flags[s] & 1);
-            if (lane == 0) s_mask[it & 3][r >> 5] = votes;
-            if constexpr (AFF) {
+          for (int i = 0; i < NACC; ++i) acc[ht][i][0] = acc[ht][i][1] = acc[ht][i][2] = acc[ht][i][3] = 0.0f;
+        if constexpr (KB == 4) {
 #pragma unroll
-              for (int i = 0; i < 2 * NG; ++i) sm_meta[((it & 3) * 2 * NG + i) * 128 + r] = meta[s][i];
-            }
-            if (flags[s] & 4) {
-              // The unit's queries: each head brought under one by a power of two (bf16's range),
-              // then fp16 part in rows 0-7 and residual in rows 8-15 of the tile.
-              ++unit;
-              const int h = r / (D / 8), c = r % (D / 8);
-              const bool bf = a.io_dtype == KVQ_DTYPE_BF16;
-              auto pair = [&](uint32_t x) {
-                return bf ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)) : __half22float2(u2h(x));
-              };
-              float2 f[4] = {pair(qw[s].x), pair(qw[s].y), pair(qw[s].z), pair(qw[s].w)};
-              float big = 0.0f;
+          for (int pb = 0; pb < NB; ++pb) {
+            __half2 h0[4], h1[4];
+            nibbles_to_h2<kOff>(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * pb + 4 * t)), h0);
+            nibbles_to_h2<kOff>(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * pb + 4 * t)), h1);
+            const uint32_t ka0[4] = {h2u(h0[0]), h2u(h1[0]), h2u(h0[2]), h2u(h1[2])};
+            const uint32_t ka1[4] = {h2u(h0[1]), h2u(h1[1]), h2u(h0[3]), h2u(h1[3])};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
-#pragma unroll
-              for (int o = 1; o < D / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-              int e = 0;
-              if (big > 0.0f && big < __int_as_float(0x7f800000)) frexpf(big, &e);
-              e = max(min(e, 126), -126);
-              const float down = __int_as_float((127 - e) << 23);
-              float sum = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                f[i] = make_float2(f[i].x * down, f[i].y * down);
-                sum += f[i].x + f[i].y;
-              }
-              // sums over each scale group of keys
-              const int width = D / kng / 8;
-#pragma unroll
-              for (int o = 1; o < D / 8; o <<= 1)
-                if (o < width) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              if (r < D) {
-                if (c % width == 0) s_qsum[unit & 3][h][c / width] = sum;
-                if (c == 0) s_qmul[unit & 3][h] = __int_as_float((127 + e) << 23) * a.qscale;
-                if (KB == 4) {   // as the codes come: 0 4 1 5 2 6 3 7
-                  const float2 t0 = f[0], t1 = f[1], t2 = f[2], t3 = f[3];
-                  f[0] = make_float2(t0.x, t2.x);
-                  f[1] = make_float2(t0.y, t2.y);
-                  f[2] = make_float2(t1.x, t3.x);
-                  f[3] = make_float2(t1.y, t3.y);
-                }
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const __half2 h2 = __floats2half2_rn(f[i].x, f[i].y);
-                  const float2 g = __half22float2(h2);
-                  hi[i] = h2u(h2);
-                  lo[i] = h2u(__floats2half2_rn(f[i].x - g.x, f[i].y - g.y));
-                }
-                uint8_t* qt = smem + S::oQ + (unit & 1) * S::kQTile + (c >> 3) * 2048;
-                *reinterpret_cast<uint4*>(qt + h * 128 + (((c ^ h) & 7) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(qt + (8 + h) * 128 + (((c ^ h) & 7) << 4)) =
-                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
+            for (int ht = 0; ht < HT; ++ht) {
+              mma_f16(acc[ht][pb], ka0, qf[ht][2 * pb][0], qf[ht][2 * pb][1]);
+              mma_f16(acc[ht][pb], ka1, qf[ht][2 * pb + 1][0], qf[ht][2 * pb + 1][1]);
             }
           }
-          const uint32_t stall = keys && it == 0 && r == 0 ? a.stall_tx : 0u;
-          if (!AFF && (flags[s] & 2)) {
-            const int box = min(p.page, 32);   // the warp's 32 rows: one box, or two on pages of 16
-            fence_async_smem();
-            if (lane == 0) mbar_expect_tx(&full[stg], 32 * ROW + stall);
-            else mbar_arrive(&full[stg]);
-            __syncwarp();
-            if (lane % box == 0) {
+        } else if constexpr (KB == 8) {
 #pragma unroll
-              for (int h = 0; h < S::kHalves; ++h)
-                tma_columns(tile + h * 16384 + r * 128, map, h * 128, (int)row[s], &full[stg]);
+          for (int ks = 0; ks < KS; ++ks) {
+            __half2 l0, h0, l1, h1;
+            signed_bytes(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * ks + 4 * t)), l0, h0);
+            signed_bytes(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * ks + 4 * t)), l1, h1);
+            const uint32_t ka[4] = {h2u(l0), h2u(l1), h2u(h0), h2u(h1)};
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht) mma_f16(acc[ht][ks >> 1], ka, qf[ht][ks][0], qf[ht][ks][1]);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint2 v0 = *reinterpret_cast<const uint2*>(kst + swz_off<ROW>(rk[0], 32 * ks + 8 * t));
+            const uint2 v1 = *reinterpret_cast<const uint2*>(kst + swz_off<ROW>(rk[1], 32 * ks + 8 * t));
+            const uint32_t ka[4] = {v0.x, v1.x, v0.y, v1.y};
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht) mma_f16(acc[ht][0], ka, qf[ht][ks][0], qf[ht][ks][1]);
+          }
+        }
+        // s * sum(q u') + z' * sum(q) per scale group of 32, 64 or 128 channels
+        bool vk[2];
+        float sc[NS][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          vk[e] = !MASK || rk[e] < nv;
+          float2 sz[NB];
+          if constexpr (AFF) {
+            const uint8_t* mrow = kmt + rk[e] * (4 * kng);
+            uint32_t ws[4] = {0u, 0u, 0u, 0u};
+            if (kng == 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(mrow);
+              ws[0] = w.x; ws[1] = w.y; ws[2] = w.z; ws[3] = w.w;
+            } else if (kng == 2) {
+              const uint2 w = *reinterpret_cast<const uint2*>(mrow);
+              ws[0] = w.x; ws[1] = w.y;
+            } else {
+              ws[0] = *reinterpret_cast<const uint32_t*>(mrow);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              sz[j] = __half22float2(u2h(ws[j]));
+              sz[j].y = fmaf((float)kOff, sz[j].x, sz[j].y);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            // the head's column (a pair's second one holds nothing)
+            auto got = [&](int nb) { return acc[M == kTwoTiles ? s : 0][nb][2 * e + (M == kSingles ? s : 0)]; };
+            float v = 0.0f;
+            if constexpr (AFF) {
+              float x[NB];
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) x[nb] = got(nb);
+              if (kng == 4) {
+#pragma unroll
+                for (int j = 0; j < NB; ++j) v = fmaf(sz[j].x, x[j], fmaf(sz[j].y, qg[s][j], v));
+              } else if (kng == 2) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  v = fmaf(sz[j].x, NB == 4 ? x[2 * j] + x[2 * j + 1] : x[j], fmaf(sz[j].y, qg[s][j], v));
+              } else {
+#pragma unroll
+                for (int j = 1; j < NB; ++j) x[0] += x[j];
+                v = fmaf(sz[0].x, x[0], sz[0].y * qg[s][0]);
+              }
+            } else {
+              v = got(0);
+            }
+            sc[s][e] = vk[e] ? v * qmul[s] : neg_inf();
+          }
+        }
+        // online softmax (log2); the block's first row is live
+        float pr[NS][2];
+        bool over = false;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) over |= fmaxf(sc[s][0], sc[s][1]) > m_run[s];
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            float mb = fmaxf(sc[s][0], sc[s][1]);
+            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 4));
+            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
+            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
+            const float mn = fmaxf(m_run[s], mb);
+            if (mn > m_run[s]) {
+              const float alpha = fast_exp2(m_run[s] - mn);
+              l_part[s] *= alpha;
+              zacc[s] *= alpha;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (M == kSingles) {
+                  oacc[0][mt][s] *= alpha;
+                  oacc[0][mt][2 + s] *= alpha;
+                } else {
+                  constexpr int kNone = 0;
+                  float(&o)[4] = oacc[M == kTwoTiles ? s : kNone][mt];
+                  o[0] *= alpha; o[1] *= alpha; o[2] *= alpha; o[3] *= alpha;
+                }
+              }
+              m_run[s] = mn;
+            }
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const float base = m_run[s] == neg_inf() ? 0.0f : m_run[s];   // scores of -inf alone weigh nothing
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            pr[s][e] = fast_exp2(sc[s][e] - base);
+            l_part[s] += pr[s][e];
+          }
+        }
+        // Rows past the end hold whatever the page holds: weight 0, and scale and
+        // zero (or fp16 values) zeroed so that no NaN reaches the products.
+        bool vok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vok[i] = !MASK || rr[i] < nv;
+        __half2 sAB = u2h(0u), zAB = u2h(0u), sCD = u2h(0u), zCD = u2h(0u);
+        if constexpr (AFF) {
+          const uint32_t* vm = reinterpret_cast<const uint32_t*>(vmt);
+          if (vfold) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float2 sz = __half22float2(u2h(vm[rk[e]]));
+              if (!vk[e]) sz = make_float2(0.0f, 0.0f);
+              sz.y = fmaf((float)kOff, sz.x, sz.y);
+#pragma unroll
+              for (int s = 0; s < NS; ++s) {
+                zacc[s] = fmaf(pr[s][e], sz.y, zacc[s]);
+                pr[s][e] *= sz.x;
+              }
             }
           } else {
-            if constexpr (AFF) {
+            uint32_t w[4];
 #pragma unroll
-              for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(tile + tile_off(r, c)) = integers<KB>(raw[s], c);
-            } else {
-              const uint4* src = reinterpret_cast<const uint4*>(side.codes + row[s] * ROW);
-#pragma unroll 4
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(tile + tile_off(r, c)) = (flags[s] & 1) ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_async_smem();
-            if (stall) mbar_expect_tx(&full[stg], stall);
-            else mbar_arrive(&full[stg]);
+            for (int i = 0; i < 4; ++i) w[i] = vok[i] ? vm[rr[i] * vng + vgi] : 0u;
+            sAB = u2h(__byte_perm(w[0], w[1], 0x5410u));
+            zAB = u2h(__byte_perm(w[0], w[1], 0x7632u));
+            sCD = u2h(__byte_perm(w[2], w[3], 0x5410u));
+            zCD = u2h(__byte_perm(w[2], w[3], 0x7632u));
           }
-          fetch(s);
+        }
+        uint32_t pb[HT][2];
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+          if constexpr (M == kSingles) {
+            pb[ht][0] = movmatrix_t(h2u(__floats2half2_rn(pr[0][0], pr[1][0])));
+            pb[ht][1] = movmatrix_t(h2u(__floats2half2_rn(pr[0][1], pr[1][1])));
+          } else {
+            const __half2 ph = __floats2half2_rn(pr[ht][0], pr[ht][1]);
+            const float2 pf = __half22float2(ph);
+            const __half2 pl = __floats2half2_rn(pr[ht][0] - pf.x, pr[ht][1] - pf.y);
+            pb[ht][0] = movmatrix_t(h2u(__lows2half2(ph, pl)));
+            pb[ht][1] = movmatrix_t(h2u(__highs2half2(ph, pl)));
+          }
+        }
+        constexpr int NWT = VTB / 4;
+        constexpr int NW = NWT > 4 ? 4 : NWT;
+#pragma unroll
+        for (int w0 = 0; w0 < NWT; w0 += NW) {
+          if (w0 > 0) asm volatile("" ::: "memory");   // the next run's loads stay behind these products
+          uint32_t A[NW], B[NW], C[NW], E[NW];
+          lds_row_words<ROW, NW>(A, vst, rr[0], g * VTB + 4 * w0);
+          lds_row_words<ROW, NW>(B, vst, rr[1], g * VTB + 4 * w0);
+          lds_row_words<ROW, NW>(C, vst, rr[2], g * VTB + 4 * w0);
+          lds_row_words<ROW, NW>(E, vst, rr[3], g * VTB + 4 * w0);
+          if constexpr (KB == 16) {
+            if (MASK) {
+#pragma unroll
+              for (int w = 0; w < NW; ++w) {
+                A[w] = vok[0] ? A[w] : 0u;
+                B[w] = vok[1] ? B[w] : 0u;
+                C[w] = vok[2] ? C[w] : 0u;
+                E[w] = vok[3] ? E[w] : 0u;
+              }
+            }
+          }
+          const int mo = w0 * (MT / NWT);
+          if (AFF && !vfold) value_products<KB, HT, NW, MT, true>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
+          else value_products<KB, HT, NW, MT, false>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
+        }
+      };
+      const bool take = blk < nv && !s_fail && !((s_bad[stg] >> (warp & 3)) & 1);   // warp-uniform
+      if (take) {
+        if (blk + 16 <= nv) block(std::false_type{});
+        else block(std::true_type{});
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stg]);
+
+      // ---- the unit's last tile here: join the warps' states, write, start over
+      const bool ends = u.j + 1 == u.tiles;
+      if (ends || it + 1 == ntile) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            l_part[s] += __shfl_xor_sync(0xffffffffu, l_part[s], o);
+            zacc[s] += __shfl_xor_sync(0xffffffffu, zacc[s], o);
+          }
+          const int head = head_of(s);
+          constexpr int kNone = 0;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const float(&o)[4] = oacc[M == kTwoTiles ? s : kNone][mt];
+            sm_acc[warp][head][(2 * mt) * 8 + g] = (M == kSingles ? o[s] : o[0] + o[1]) + zacc[s];
+            sm_acc[warp][head][(2 * mt + 1) * 8 + g] = (M == kSingles ? o[2 + s] : o[2] + o[3]) + zacc[s];
+          }
+          if (g == 0) {
+            sm_m[warp][head] = m_run[s];
+            sm_l[warp][head] = l_part[s];
+          }
+        }
+        named_sync(1, 32 * NCW);
+        const bool final = !a.joined && begun_here && ends;
+        const long long unit = (long long)u.b * p.Hkv + u.kvh;
+        // a warp a head: lane i holds channels D / 32 * i on
+#pragma unroll 1
+        for (int head = warp; head < a.G; head += NCW) {
+          const int i = lane;
+          float mm = neg_inf(), ll = 0.0f, w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mm = fmaxf(mm, sm_m[k][head]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = sm_l[k][head] == 0.0f ? 0.0f : fast_exp2(sm_m[k][head] - mm);
+            ll = fmaf(sm_l[k][head], w[k], ll);
+          }
+          constexpr int C = D / 32;
+          float o[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int d = (i & 31) * C + c;
+            o[c] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (w[k] != 0.0f) o[c] = fmaf(w[k], sm_acc[k][head][(d % VCH) * 8 + d / VCH], o[c]);
+          }
+          if (final) {
+            const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+            const size_t at = ((size_t)u.b * a.Hq + (size_t)u.kvh * a.G + head) * D + (i & 31) * C;
+#pragma unroll
+            for (int c = 0; c < C; ++c) store_io(a.out, at + c, a.io_dtype, o[c] * r);
+          } else {
+            float* dst = a.parts + ((size_t)(blockIdx.x + unit) * a.G + head) * (D + kPartPad);
+#pragma unroll
+            for (int c = 0; c < C; ++c) dst[(i & 31) * C + c] = o[c];
+            if ((i & 31) == 0) {
+              dst[D] = mm;
+              dst[D + 1] = ll;
+            }
+          }
+        }
+        named_sync(1, 32 * NCW);
+        clear();
+        first = true;
+      }
+      if (++u.j == u.tiles) {
+        u.j = 0;
+        begun_here = true;
+        if (++u.kvh == p.Hkv) {
+          u.kvh = 0;
+          if (it + 1 < ntile) {
+            do {
+              ++u.b;
+              u.tiles = sm_start[u.b + 1] - sm_start[u.b];
+            } while (u.tiles == 0);
+            own_len = part_of(a.batch.lens[u.b], a.batch.max_pages, p.page_log2, nullptr).len;
+          }
         }
       }
     }
-    // no copy is left in flight when the CTA ends, whatever else ran out
-    if (!AFF)
-      for (int it = max(ntile - NST, 0); it < ntile; ++it) mbar_wait_bounded(&full[it % NST], (it / NST) & 1);
-  } else if (lane == 0) {
-    // ------------------------------------------------------------ products
-    constexpr uint32_t kQK = mma_desc(128, 16, false, false);
-    const uint32_t kPV = mma_desc(128, (D == 64 ? 32 : 16) * vng, true, true);
-    const int gsteps = D / 16 / kng;   // k-steps of a scale group of keys
-    int unit = -1;
-    At w = u;   // the next tile to be scored
-    auto scores = [&](int it) {
-      const int stg = it % NST;
-      if (w.j == 0 || it == 0) ++unit;
-      wait(&k_full[stg], (it / NST) & 1);
-      tc_fence_after();
-      const uint32_t ka = smem_u32(smem + S::oK + stg * S::kTile), qa = smem_u32(smem + S::oQ + (unit & 1) * S::kQTile);
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t in = (k & 3) * 32;
-        tc_mma_ss(tmem + (it & 1) * scols + 16 * (k / gsteps), operand_desc(ka + (k >> 2) * 16384 + in, 16, 1024),
-                  operand_desc(qa + (k >> 2) * 2048 + in, 16, 1024), kQK, k % gsteps > 0);
-      }
-      tc_commit(&s_full[it & 1]);
-      tc_commit(&k_empty[stg]);
-      step(w);
-    };
-    scores(0);
-    if (ntile > 1) scores(1);
-    At v = u;   // the tile whose values come next
-    for (int it = 0; it < ntile; ++it) {
-      const int stg = it % NST;
-      const bool begins = v.j == 0 || it == 0;
-      wait(&p_full[it & 1], (it >> 1) & 1);
-      wait(&v_full[stg], (it / NST) & 1);
-      tc_fence_after();
-      const uint32_t va = smem_u32(smem + S::oV + stg * S::kTile), pa = smem_u32(smem + S::oP + (it & 1) * S::kP);
-      const uint32_t lead_p = (D == 64 ? 2 : 1) * 2 * vng * 128;   // bytes of eight rows of weights
-#pragma unroll
-      for (int k = 0; k < (D == 64 ? 4 : 8); ++k)
-        tc_mma_ss(tmem_o, operand_desc(va + k * 2048, D == 64 ? 8192 : 16384, 1024),
-                  operand_desc(pa + k * 2 * lead_p, lead_p, 128, kPlain), kPV, !begins || k > 0);
-      tc_commit(&v_empty[stg]);
-      if (it + 2 < ntile) scores(it + 2);
-      step(v);
-    }
-    // the last product is done before the tensor memory goes back
-    mbar_wait_bounded(&v_empty[(ntile - 1) % NST], ((ntile - 1) / NST) & 1);
   }
   __syncthreads();
-  tc_fence_after();
-  if (warp == 12) tmem_free(tmem, kCols);
-  if (s_fail && threadIdx.x == 0) set_pool_status(p.status, KVQ_DEV_TIMEOUT);
+  if (s_fail && threadIdx.x == 0) {
+    // a stage never arrived: say so, and wait (bounded) for the copies still in flight
+    set_pool_status(p.status, KVQ_DEV_TIMEOUT);
+    for (int s = 0; s < NST; ++s)
+      if (s_issued[s] >= 0) mbar_wait_bounded(&full[s], s_issued[s]);
+  }
   if (a.joined && lead) grid_dependency_wait();
 }
 

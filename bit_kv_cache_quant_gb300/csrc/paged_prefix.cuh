@@ -27,9 +27,11 @@
 // with the softmax scale.
 #pragma once
 
-#include "paged_tc.cuh"
+#include "paged_own.cuh"
 
 namespace kvq {
+
+constexpr float kSlack = 8.0f;
 
 struct PrefixArgs {
   BatchView batch;
@@ -47,6 +49,96 @@ struct PrefixArgs {
 // CTAs that share a prefix of `tiles` tiles.
 __device__ __forceinline__ int prefix_runs(int tiles, int nsplit) { return tiles < nsplit ? tiles : nsplit; }
 
+// ------------------------------------------------------------- tensor memory --
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* m) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(m))
+               : "memory");
+}
+// Waits for the loads into r (and all before them); r is an operand, so that no use of it moves up past the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
+      "%31,%32};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle; strides in bytes.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor of kind::f16: fp16 operands, fp32 accumulators, A rows along K; b_mn: B along N.
+__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// 128 bytes of TMA box columns from byte x of rows y .. of a 2-d code-plane map.
+__device__ __forceinline__ void tma_columns(void* dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(m))
+      : "memory");
+}
+
 template <int D, int F, int NQ> struct PrefixShape {
   static constexpr int kHalves = D / 64;             // 64-channel halves of a row, 128 bytes each
   static constexpr int kTile = 128 * D * 2;          // a 128-row fp16 tile
@@ -57,6 +149,38 @@ template <int D, int F, int NQ> struct PrefixShape {
   static constexpr int kThreads = 32 * (kMma + 1);
   static constexpr uint32_t kCols = 512;             // tensor memory: 128 S + 128 O per stream
 };
+
+// Byte offset of 16-byte chunk c (of D / 8) of row r in a swizzled tile.
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  return (uint32_t)((c >> 3) * 16384 + r * 128 + (((c ^ r) & 7) << 4));
+}
+
+// Decodes 16-byte-chunk-ordered fp16 of one stored row from its raw words: chunk c
+// holds channels 8 c .. 8 c + 7, for 4-bit codes in the order 0 4 1 5 2 6 3 7
+// (queries are laid out, and outputs read, the same way).
+template <int D, int F>
+__device__ __forceinline__ void store_decoded(uint8_t* tile, int r, const uint32_t* raw, const uint32_t* meta, int ng) {
+  constexpr int KB = FmtBits<F>::v;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    uint4 o;
+    {
+      // the chunk's (scale, zero): the groups of a row are 32, 64 or 128 channels
+      const uint32_t m = ng == 1 ? meta[0] : (ng == D / 64 ? meta[c >> 3] : meta[c >> 2]);
+      const __half2 s = u2h(__byte_perm(m, m, 0x1010u)), z = u2h(__byte_perm(m, m, 0x3232u));
+      __half2 h[4];
+      if constexpr (KB == 4) {
+        nibbles_to_h2(raw[c], h);
+      } else {
+        bytes_to_h2(raw[2 * c] ^ 0x80808080u, h[0], h[1]);
+        bytes_to_h2(raw[2 * c + 1] ^ 0x80808080u, h[2], h[3]);
+      }
+      o = make_uint4(h2u(__hfma2(h[0], s, z)), h2u(__hfma2(h[1], s, z)), h2u(__hfma2(h[2], s, z)),
+                     h2u(__hfma2(h[3], s, z)));
+    }
+    *reinterpret_cast<uint4*>(tile + tile_off(r, c)) = o;
+  }
+}
 
 // Registers a thread (of 96 at launch: 8 warps give 32 each to 8 others).
 template <int N> __device__ __forceinline__ void raise_registers() {
@@ -387,7 +511,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
       for (int j = max(n - NST, 0); j < n; ++j) mbar_wait_bounded(&full[j % NST], (j / NST) & 1);
   } else if (lane == 0) {
     // ------------------------------------------------------------ products
-    constexpr uint32_t kQK = mma_desc(128, 128, false, false), kPV = mma_desc(128, D, false, true);
+    constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
     auto scores = [&](int t, int j) {   // S of stream t = its queries against keys of tile j
       const uint32_t qa = smem_u32(sq + (NQ == 2 ? t : 0) * S::kTile), ka = smem_u32(sk + (j % NST) * S::kTile);
 #pragma unroll
