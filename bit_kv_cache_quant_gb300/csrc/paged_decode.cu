@@ -6,78 +6,93 @@ namespace kvq {
 
 namespace {
 
-// Joins a unit's states with the online-softmax rule, one warp per query
-// head: those of the CTAs that had tiles of it and, where the prefix was
-// taken for the whole batch, those of the prefix's runs.  A unit that one CTA
-// finished is left alone; one without rows gets zeros.
+// Joins a unit's states with the online-softmax rule, two warps per query
+// head, each half of the states: those of the CTAs that had tiles of it and,
+// where the prefix was taken for the whole batch, those of the prefix's
+// streams.  A unit that one CTA finished is left alone; one without rows gets
+// zeros.  Bound by the latency of its few dependent loads: 64 sequences of 32
+// heads and 19 states each, 20 MB from L2.
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const OwnArgs a, const PrefixArgs f, int Hkv, int grid,
+__global__ void __launch_bounds__(512) paged_merge_kernel(const OwnArgs a, const PrefixArgs f, int Hkv, int grid,
                                                           int page_log2) {
   constexpr int C = D / 32;
+  __shared__ float sm_l[8], sm_acc[8][D];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >= a.G, h = part ? warp - a.G : warp;
   const int unit = blockIdx.x, b = unit / Hkv, kvh = unit - b * Hkv;
+  const int start = a.starts[b], tiles = a.starts[b + 1] - start;
   const long long total = (long long)a.starts[a.batch.n_seqs] * Hkv;
-  const int tiles = a.starts[b + 1] - a.starts[b];
-  const long long x0 = (long long)a.starts[b] * Hkv + (long long)kvh * tiles, x1 = x0 + tiles - 1;
-  const int ctas = busy_ctas(total, grid);
-  int c0 = 0, n = 0;
-  if (tiles > 0) {   // CTA c takes the tiles from total * c / ctas on
-    c0 = (int)(((x0 + 1) * ctas + total - 1) / total) - 1;
-    n = (int)(((x1 + 1) * ctas + total - 1) / total) - c0;
-  }
-  if (n == 1 && !a.joined) return;
   int runs = 0;
   if (a.joined) {
     const Part pre = part_of(a.batch.prefix_len[0], a.batch.max_prefix_pages, page_log2, nullptr);
     runs = prefix_runs((pre.len + 127) >> 7, f.nsplit) * f.streams;
   }
+  int c0 = 0, n = 0;
+  if (tiles > 0) {   // CTA c takes the tiles from total * c / ctas on
+    const int ctas = busy_ctas(total, grid);
+    const long long x0 = (long long)start * Hkv + (long long)kvh * tiles, x1 = x0 + tiles - 1;
+    if (total * ctas < (1ll << 32)) {
+      c0 = (int)(((uint32_t)(x0 + 1) * ctas + (uint32_t)total - 1) / (uint32_t)total) - 1;
+      n = (int)(((uint32_t)(x1 + 1) * ctas + (uint32_t)total - 1) / (uint32_t)total) - c0;
+    } else {
+      c0 = (int)(((x0 + 1) * ctas + total - 1) / total) - 1;
+      n = (int)(((x1 + 1) * ctas + total - 1) / total) - c0;
+    }
+  }
+  if (n == 1 && !a.joined) return;   // (the whole block)
   const float* own = a.parts + ((size_t)(c0 + unit) * a.G + h) * (D + kPartPad);
   const size_t stride = (size_t)a.G * (D + kPartPad);
   const size_t run0 = (size_t)kvh * f.nsplit * f.streams * f.rows + (size_t)b * a.G + h;   // + run * f.rows
+  // state i: an own one, or a prefix stream's; this warp's are part, part + 2, ...
+  const int count = n + runs;
+  auto state = [&](int i) {
+    return i < n ? make_float2(own[i * stride + D], own[i * stride + D + 1]) : f.part_ml[run0 + (size_t)(i - n) * f.rows];
+  };
+  auto rows_of = [&](int i) { return i < n ? own + i * stride : f.part_o + (run0 + (size_t)(i - n) * f.rows) * D; };
   float m = neg_inf();
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, own[i * stride + D]);
-  for (int i = lane; i < runs; i += 32) m = fmaxf(m, f.part_ml[run0 + (size_t)i * f.rows].x);
+  for (int i = lane; i < count; i += 32) m = fmaxf(m, state(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   // Weights first, a lane a state; then the states' rows, several in flight.
   float l = 0.0f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-  auto join = [&](int count, auto state, auto rows_of) {   // state(i): (max, sum); rows_of(i): the D accumulators
-    for (int i0 = 0; i0 < count; i0 += 32) {
-      float wi = 0.0f;
-      if (i0 + lane < count) {
-        const float2 ml = state(i0 + lane);
-        if (ml.y != 0.0f) {   // sum 0: no live row
-          wi = fast_exp2(ml.x - m);
-          l = fmaf(ml.y, wi, l);
-        }
-      }
-      const int cnt = min(32, count - i0);
-#pragma unroll 8
-      for (int i = 0; i < cnt; ++i) {
-        const float w = __shfl_sync(0xffffffffu, wi, i);
-        const float* s = rows_of(i0 + i) + lane * C;
-        float x[C];
-        if constexpr (C == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(s);
-        else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(s);
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = w == 0.0f ? acc[c] : fmaf(w, x[c], acc[c]);
+  for (int i0 = part; i0 < count; i0 += 64) {
+    float wi = 0.0f;
+    if (i0 + 2 * lane < count) {
+      const float2 ml = state(i0 + 2 * lane);
+      if (ml.y != 0.0f) {   // sum 0: no live row
+        wi = fast_exp2(ml.x - m);
+        l = fmaf(ml.y, wi, l);
       }
     }
-  };
-  join(n, [&](int i) { return make_float2(own[i * stride + D], own[i * stride + D + 1]); },
-       [&](int i) { return own + i * stride; });
-  join(runs, [&](int i) { return f.part_ml[run0 + (size_t)i * f.rows]; },
-       [&](int i) { return f.part_o + (run0 + (size_t)i * f.rows) * D; });
+    const int cnt = min(32, (count - i0 + 1) >> 1);
+#pragma unroll 10
+    for (int i = 0; i < cnt; ++i) {
+      const float* s = rows_of(i0 + 2 * i) + lane * C;
+      float x[C];
+      if constexpr (C == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(s);
+      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(s);
+      const float w = __shfl_sync(0xffffffffu, wi, i);
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = w == 0.0f ? acc[c] : fmaf(w, x[c], acc[c]);
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (part) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) sm_acc[h][lane * C + c] = acc[c];
+    if (lane == 0) sm_l[h] = l;
+  }
+  __syncthreads();
+  if (part) return;
+  l += sm_l[h];
   const float r = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t at = ((size_t)b * a.Hq + (size_t)kvh * a.G + h) * D + lane * C;
 #pragma unroll
-  for (int c = 0; c < C; ++c) store_io(a.out, at + c, a.io_dtype, acc[c] * r);
+  for (int c = 0; c < C; ++c) store_io(a.out, at + c, a.io_dtype, (acc[c] + sm_acc[h][lane * C + c]) * r);
 }
 
 size_t starts_bytes(int n_seqs) { return ((size_t)(n_seqs + 1) * 4 + 255) / 256 * 256; }
@@ -160,7 +175,7 @@ cudaError_t launch_own(const PoolView& p, const OwnArgs& a, const PrefixArgs& f,
   e = cudaLaunchKernelEx(&cfg, kern, p, a);
   if (e != cudaSuccess) return e;
   note_launch();
-  cfg = dependent_launch(dim3(a.batch.n_seqs * p.Hkv), 32 * a.G, 0, st, &at);
+  cfg = dependent_launch(dim3(a.batch.n_seqs * p.Hkv), 64 * a.G, 0, st, &at);
   e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, a, f, p.Hkv, (int)ctas, p.page_log2);
   note_launch();
   return e;

@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           vk[e] = !MASK || rk[e] < nv;
-          float2 sz[NB];
+          [[maybe_unused]] float2 sz[NB];
           if constexpr (AFF) {
             const uint8_t* mrow = kmt + rk[e] * (4 * kng);
             uint32_t ws[4] = {0u, 0u, 0u, 0u};

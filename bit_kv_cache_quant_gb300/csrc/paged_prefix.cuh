@@ -14,9 +14,10 @@
 // bring keys and the four after them values into shared
 // memory in the order the matrix unit wants (128-byte swizzle): fp16 pages by
 // TMA, 8- and 4-bit pages (and tiles with rows to leave out) by a thread a row,
-// decoded to fp16 on the way (one rounding of u * s + z); one thread of the
-// last warp issues the products.  While one stream is in its softmax the
-// other's products run.  The loading warps hand registers to the softmax warps.
+// decoded to fp16 on the way (one rounding of u * s + z).  A stream's first
+// warp issues its products, which its warps would wait for anyway; while one
+// stream is in its softmax the other's products run.  The loading warps hand
+// registers to the softmax warps.
 //
 // The running maximum of a row moves only when a tile exceeds it by more than
 // 2^kSlack (weights up to 2^kSlack are exact enough in fp16 and fp32), so that
@@ -145,8 +146,7 @@ template <int D, int F, int NQ> struct PrefixShape {
   static constexpr int kStages = 2;                  // of keys and of values
   static constexpr int kSmem = NQ * kTile + 2 * kStages * kTile + 1024;
   static constexpr int kSoft = 8;                    // softmax warps
-  static constexpr int kMma = kSoft + 8;             // the warp that issues the products
-  static constexpr int kThreads = 32 * (kMma + 1);
+  static constexpr int kThreads = 32 * (kSoft + 8);
   static constexpr uint32_t kCols = 512;             // tensor memory: 128 S + 128 O per stream
 };
 
@@ -182,7 +182,7 @@ __device__ __forceinline__ void store_decoded(uint8_t* tile, int r, const uint32
   }
 }
 
-// Registers a thread (of 96 at launch: 8 warps give 32 each to 8 others).
+// Registers a thread: of 16 warps with 128 each, 8 go down to 88 and 8 up to 168.
 template <int N> __device__ __forceinline__ void raise_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
@@ -190,9 +190,15 @@ template <int N> __device__ __forceinline__ void lower_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 template <int D, int F, int NQ>
-__global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
-    paged_prefix_kernel(const __grid_constant__ PoolView p, const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_prefix_kernel(const __grid_constant__ PoolView p, const __grid_constant__ PrefixArgs a) {
   using S = PrefixShape<D, F, NQ>;
   constexpr int KB = FmtBits<F>::v, ROW = D * KB / 8, RAW = ROW / 4, NST = S::kStages;
   constexpr bool AFF = F != F_FP16;
@@ -201,14 +207,15 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
   uint8_t* sq = smem;
   uint8_t* sk = smem + NQ * S::kTile;
   uint8_t* sv = sk + NST * S::kTile;
-  __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], p_full[2],
-      o_full[2];
+  __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], o_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_mask[4][4];   // live rows of tile j in ring slot j & 3
   __shared__ float s_scale[NQ * 128];
   __shared__ volatile int s_fail;
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (from one lane, so that what follows from the warp's number is known to be uniform: a product's
+  // operands then live in uniform registers)
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int kvh = blockIdx.y, row0 = blockIdx.z * (128 * NQ);
   if (threadIdx.x == 0) {
     s_fail = 0;
@@ -216,12 +223,11 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
     for (int i = 0; i < NST; ++i) {
       mbar_init(&k_full[i], 128);
       mbar_init(&v_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&k_empty[i], NQ);   // streams that read the tile
+      mbar_init(&v_empty[i], NQ);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
     }
     fence_mbar_init();
@@ -235,11 +241,11 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
   if ((int)blockIdx.x >= runs) return;   // the whole CTA, before any tensor memory is held
   const int j0 = (int)((long long)tiles * blockIdx.x / runs), j1 = (int)((long long)tiles * (blockIdx.x + 1) / runs);
   const int n = j1 - j0;
-  if (warp == S::kMma) tmem_alloc(&s_tmem, S::kCols);
+  if (warp == S::kSoft + 7) tmem_alloc(&s_tmem, S::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   // every wait is bounded; once one runs out the others return at once, the loops
   // keep their counts and the results are marked by the status word
   auto wait = [&](uint64_t* m, uint32_t parity) {
@@ -248,14 +254,42 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
 
   if (warp < S::kSoft) {
     // ------------------------------------------------------------- softmax
-    raise_registers<128>();
+    raise_registers<168>();
     const int t = warp >> 2;                       // the stream
     const int qt = NQ == 2 ? t : 0;                // its row tile
     const int mine_n = NQ == 2 ? n : (n + 1 - t) >> 1;   // its tiles
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, lane number from bit 16 on
     const uint32_t ts = tmem + lanes + t * 256, to = ts + 128;
     const int r = (warp & 3) * 32 + lane;
+    // Products are issued by the stream's first warp, when its four warps have met.
+    constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
+    const uint64_t qd = operand_desc(smem_u32(sq + qt * S::kTile), 16, 1024);
+    auto scores = [&](int j) {   // S = the stream's queries against keys of tile j
+      const uint64_t kd = operand_desc(smem_u32(sk + (j % NST) * S::kTile), 16, 1024);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+        tc_mma_ss(tmem + t * 256, qd + off, kd + off, kQK, k > 0);
+      }
+      tc_commit(&s_full[t]);
+      tc_commit(&k_empty[j % NST]);
+    };
+    auto values = [&](int j, bool add) {   // O += the weights times values of tile j
+      const uint64_t vd = operand_desc(smem_u32(sv + (j % NST) * S::kTile), 16384, 1024);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + 64 + 8 * k, vd + ((k * 2048) >> 4), kPV, add || k > 0);
+      tc_commit(&v_empty[j % NST]);
+    };
+    const bool leads = (warp & 3) == 0;
     wait(&q_full, 0);
+    if (leads && mine_n > 0) {
+      const int j = NQ == 2 ? 0 : t;
+      wait(&k_full[j], 0);
+      tc_fence_after();
+      if (elect_one()) scores(j);
+      __syncwarp();
+    }
     const float c = s_scale[qt * 128 + r] * a.qscale;
     float m = neg_inf(), l = 0.0f;
 #pragma unroll 1
@@ -263,66 +297,29 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
       const int j = NQ == 2 ? k : 2 * k + t;
       wait(&s_full[t], k & 1);
       tc_fence_after();
-      uint32_t live[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) live[i] = s_mask[j & 3][i];
-      // Scores in quarters of 32 columns, the next one on its way while one is used; the last
-      // stays in registers for the weights, which go to columns 64 .. 127 as those are read.
+      volatile const uint32_t* live = s_mask[j & 3];
+      // Scores in quarters of 32 columns, the next one on its way while one is used.  Weights against the
+      // row's reference maximum are kept back until all 128 scores have shown that it stands.
       uint32_t xa[32], xb[32];
       float t0 = neg_inf(), t1 = neg_inf();
+      float2 sum = make_float2(0.0f, 0.0f);
+      const float2 c2 = make_float2(c, c);
       auto mask = [&](uint32_t(&x)[32], int i) {
-        if (live[i] != 0xffffffffu) {
+        const uint32_t word = live[i];
+        if (word != 0xffffffffu) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (!((live[i] >> e) & 1)) x[e] = 0xff800000u;
+            if (!((word >> e) & 1)) x[e] = 0xff800000u;
         }
       };
-      auto highest = [&](uint32_t(&x)[32], int i) {
-        mask(x, i);
+      auto highest = [&](uint32_t(&x)[32]) {
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           t0 = fmaxf(fmaxf(t0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
           t1 = fmaxf(fmaxf(t1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
         }
       };
-      tmem_ld32(xa, ts);
-      tmem_wait_ld(xa);
-      tmem_ld32(xb, ts + 32);
-      highest(xa, 0);
-      tmem_wait_ld(xb);
-      tmem_ld32(xa, ts + 64);
-      highest(xb, 1);
-      tmem_wait_ld(xa);
-      tmem_ld32(xb, ts + 96);
-      highest(xa, 2);
-      tmem_wait_ld(xb);
-      highest(xb, 3);
-      float top = fmaxf(t0, t1);
-      top *= c;
-      const float lift = k == 0 ? 0.0f : kSlack;
-      if (__any_sync(0xffffffffu, top > m + lift)) {
-        const bool up = top > m + lift;
-        const float mn = up ? top : m;
-        const float alpha = up ? fast_exp2(m - mn) : 1.0f;
-        if (k > 0) {   // (the first tile's product overwrites the accumulators)
-          l *= alpha;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t y[32];
-            tmem_ld32(y, to + 32 * i);
-            tmem_wait_ld(y);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
-            tmem_st32(to + 32 * i, y);
-          }
-        }
-        m = mn;
-      }
-      const float base = m == neg_inf() ? 0.0f : m;   // no live row yet: every weight is 2^-inf
-      float2 sum = make_float2(0.0f, 0.0f);
-      const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
-      auto weigh = [&](uint32_t(&x)[32], int i) {
-        uint32_t w[16];
+      auto weigh = [&](uint32_t(&x)[32], uint32_t* w, float2 base2) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 v = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, base2);
@@ -331,27 +328,99 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
           sum = add2(sum, v);
           w[e] = h2u(__floats2half2_rn(v.x, v.y));
         }
-        tmem_st16(ts + 64 + 16 * i, w);
       };
-      tmem_ld32(xa, ts + 64);
-      weigh(xb, 3);
-      tmem_wait_ld(xa);
-      tmem_ld32(xb, ts);
-      mask(xa, 2);
-      weigh(xa, 2);
-      tmem_wait_ld(xb);
-      tmem_ld32(xa, ts + 32);
-      mask(xb, 0);
-      weigh(xb, 0);
-      tmem_wait_ld(xa);
-      mask(xa, 1);
-      weigh(xa, 1);
+      bool stands = k > 0;
+      if (stands) {   // (the same for the whole warp)
+        uint32_t w0[32], w1[32];
+        const float base = m == neg_inf() ? 0.0f : m;
+        const float2 base2 = make_float2(-base, -base);
+        tmem_ld32(xa, ts);
+        tmem_wait_ld(xa);
+        tmem_ld32(xb, ts + 32);
+        mask(xa, 0);
+        highest(xa);
+        weigh(xa, w0, base2);
+        tmem_wait_ld(xb);
+        tmem_ld32(xa, ts + 64);
+        mask(xb, 1);
+        highest(xb);
+        weigh(xb, w0 + 16, base2);
+        tmem_wait_ld(xa);
+        tmem_ld32(xb, ts + 96);
+        mask(xa, 2);
+        highest(xa);
+        weigh(xa, w1, base2);
+        tmem_wait_ld(xb);
+        mask(xb, 3);
+        highest(xb);
+        weigh(xb, w1 + 16, base2);
+        stands = !__any_sync(0xffffffffu, fmaxf(t0, t1) * c > m + kSlack);
+        if (stands) {   // over scores this thread has read
+          tmem_st32(ts + 64, w0);
+          tmem_st32(ts + 96, w1);
+        }
+      }
+      if (!stands) {   // the first tile, or a new maximum: the scores are still there
+        t0 = t1 = neg_inf();
+        sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          tmem_ld32(xa, ts + 32 * i);
+          tmem_wait_ld(xa);
+          mask(xa, i);
+          highest(xa);
+        }
+        const float top = fmaxf(t0, t1) * c;
+        const bool up = top > m;
+        const float mn = up ? top : m;
+        if (k > 0) {   // (the first tile's product overwrites the accumulators)
+          const float alpha = up ? fast_exp2(m - mn) : 1.0f;
+          l *= alpha;
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            tmem_ld32(xa, to + 32 * i);
+            tmem_wait_ld(xa);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) xa[e] = __float_as_uint(__uint_as_float(xa[e]) * alpha);
+            tmem_st32(to + 32 * i, xa);
+          }
+        }
+        m = mn;
+        const float base = m == neg_inf() ? 0.0f : m;   // no live row yet: every weight is 2^-inf
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {   // quarters 3, 2, 0, 1: weights go where scores have been read twice
+          const int at = i < 2 ? 3 - i : i - 2;
+          uint32_t w[16];
+          tmem_ld32(xa, ts + 32 * at);
+          tmem_wait_ld(xa);
+          mask(xa, at);
+          weigh(xa, w, make_float2(-base, -base));
+          tmem_st16(ts + 64 + 16 * at, w);
+        }
+      }
       l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[t]);
+      named_sync(1 + t, 128);
+      if (leads) {
+        const int next = NQ == 2 ? j + 1 : j + 2;
+        const bool more = k + 1 < mine_n;
+        wait(&v_full[j % NST], (j / NST) & 1);
+        tc_fence_after();
+        if (elect_one()) {
+          values(j, k > 0);
+          if (!more) tc_commit(&o_full[t]);
+        }
+        __syncwarp();
+        if (more) {
+          wait(&k_full[next % NST], (next / NST) & 1);
+          tc_fence_after();
+          if (elect_one()) scores(next);
+        }
+      }
+      __syncwarp();
     }
-    if (mine_n > 0) wait(&o_full[t], 0);
+    if (mine_n > 0 && !mbar_wait_bounded(&o_full[t], 0)) s_fail = 1;   // the last product is done, whatever ran out
     tc_fence_after();
     const int row = row0 + qt * 128 + r;
     const bool mine = row < a.rows && !s_fail;
@@ -378,9 +447,9 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
         }
       }
     }
-  } else if (warp < S::kMma) {
+  } else {
     // -------------------------------------------- queries, keys and values
-    lower_registers<64>();
+    lower_registers<88>();
     const bool keys = warp < S::kSoft + 4;
     const int r = (threadIdx.x - 32 * S::kSoft) & 127;   // a thread a row
     if (keys || NQ == 2) {   // the key warps lay out the first row tile, the value warps the second
@@ -509,80 +578,10 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
     // no copy is left in flight when the CTA ends, whatever else ran out
     if (!AFF)
       for (int j = max(n - NST, 0); j < n; ++j) mbar_wait_bounded(&full[j % NST], (j / NST) & 1);
-  } else if (lane == 0) {
-    // ------------------------------------------------------------ products
-    constexpr uint32_t kQK = mma_desc(128, 128, false), kPV = mma_desc(128, D, true);
-    auto scores = [&](int t, int j) {   // S of stream t = its queries against keys of tile j
-      const uint32_t qa = smem_u32(sq + (NQ == 2 ? t : 0) * S::kTile), ka = smem_u32(sk + (j % NST) * S::kTile);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-        tc_mma_ss(tmem + t * 256, operand_desc(qa + off, 16, 1024), operand_desc(ka + off, 16, 1024), kQK, k > 0);
-      }
-      tc_commit(&s_full[t]);
-    };
-    auto values = [&](int t, int j, bool add) {   // O of stream t += its weights times values of tile j
-      const uint32_t va = smem_u32(sv + (j % NST) * S::kTile);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + 64 + 8 * k, operand_desc(va + k * 2048, 16384, 1024), kPV,
-                  add || k > 0);
-    };
-    auto keys_in = [&](int j) {
-      wait(&k_full[j % NST], (j / NST) & 1);
-      tc_fence_after();
-    };
-    wait(&q_full, 0);
-    if constexpr (NQ == 2) {
-      keys_in(0);
-      scores(0, 0);
-      scores(1, 0);
-      tc_commit(&k_empty[0]);
-      for (int j = 0; j < n; ++j) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          wait(&p_full[t], j & 1);
-          if (t == 0) wait(&v_full[j % NST], (j / NST) & 1);
-          tc_fence_after();
-          values(t, j, j > 0);
-          if (j + 1 == n) tc_commit(&o_full[t]);
-          if (t == 1) tc_commit(&v_empty[j % NST]);
-          if (j + 1 < n) {
-            if (t == 0) keys_in(j + 1);
-            scores(t, j + 1);
-            if (t == 1) tc_commit(&k_empty[(j + 1) % NST]);
-          }
-        }
-      }
-    } else {
-      for (int j = 0; j < 2 && j < n; ++j) {
-        keys_in(j);
-        scores(j, j);
-        tc_commit(&k_empty[j]);
-      }
-      for (int j = 0; j < n; ++j) {
-        const int t = j & 1;
-        wait(&p_full[t], (j >> 1) & 1);
-        wait(&v_full[j % NST], (j / NST) & 1);
-        tc_fence_after();
-        values(t, j, j > 1);
-        tc_commit(&v_empty[j % NST]);
-        if (j + 2 < n) {
-          keys_in(j + 2);
-          scores(t, j + 2);
-          tc_commit(&k_empty[j % NST]);
-        } else {
-          tc_commit(&o_full[t]);
-        }
-      }
-    }
-    // the last product is done before the tensor memory goes back
-    for (int t = 0; t < 2; ++t)
-      if (NQ == 2 || t < n) mbar_wait_bounded(&o_full[t], 0);
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == S::kMma) tmem_free(tmem, S::kCols);
+  if (warp == S::kSoft + 7) tmem_free(tmem, S::kCols);
   if (s_fail && threadIdx.x == 0) set_pool_status(p.status, KVQ_DEV_TIMEOUT);
 }
 
