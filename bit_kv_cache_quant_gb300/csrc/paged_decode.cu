@@ -108,7 +108,14 @@ struct Plan {
 Plan make_plan(const PoolView& p, int n_seqs, int G, int max_prefix_pages) {
   Plan r{};
   const long long rows = (long long)n_seqs * G;
-  r.shared = max_prefix_pages > 0 && n_seqs > 1;
+  // Taking the prefix once costs a launch and a longer merge; taking it with
+  // every sequence costs its tiles n_seqs times, from L2 after the first.
+  // Measured at 8 kv heads of 128, four query heads each, 64 own rows, 4-bit
+  // (once / with each, us): 4 sequences behind 4K 25 / 19, behind 16K 32 / 38;
+  // 8 behind 4K 26 / 25; 16 behind 1K 16 / 18, behind 4K 29 / 38; 64 behind 256
+  // rows 22 / 24, behind 16K 44 / 422.
+  r.shared = n_seqs > 1 &&
+             (long long)n_seqs * p.Hkv * ((((long long)max_prefix_pages << p.page_log2) + 63) >> 6) > 27LL * p.sms;
   if (!r.shared) return r;
   r.nq = rows > 128 ? 2 : 1;
   r.streams = r.nq == 2 ? 1 : 2;

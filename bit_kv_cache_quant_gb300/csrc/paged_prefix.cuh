@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
   uint8_t* sq = smem;
   uint8_t* sk = smem + NQ * S::kTile;
   uint8_t* sv = sk + NST * S::kTile;
-  __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], o_full[2];
+  __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], o_full[2],
+      issued[2];
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_mask[4][4];   // live rows of tile j in ring slot j & 3
   __shared__ float s_scale[NQ * 128];
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&o_full[i], 1);
+      mbar_init(&issued[i], 1);
     }
     fence_mbar_init();
   }
@@ -406,6 +408,10 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
         const int next = NQ == 2 ? j + 1 : j + 2;
         const bool more = k + 1 < mine_n;
         wait(&v_full[j % NST], (j / NST) & 1);
+        // The streams take turns at the matrix unit: sharing it they fall into step, both in their
+        // softmax and then both waiting for products.
+        if (t == 1) wait(&issued[0], k & 1);
+        else if (k > 0) wait(&issued[1], (k - 1) & 1);
         tc_fence_after();
         if (elect_one()) {
           values(j, k > 0);
@@ -417,6 +423,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
           tc_fence_after();
           if (elect_one()) scores(next);
         }
+        if (lane == 0) mbar_arrive(&issued[t]);
       }
       __syncwarp();
     }
