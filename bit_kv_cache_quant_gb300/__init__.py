@@ -649,8 +649,9 @@ class PagedKVCache:
     page_table [B, max_pages], seq_lens [B]: token j of sequence b is row j % page_size of page
     page_table[b, j // page_size].  prefix_pages [n], prefix_len [1]: tokens in front of every sequence.
 
-    A call on a stream other than the tensors' own, or a graph, needs its own `workspace` (workspace_bytes)
-    when it may run beside another decode_attn of this pool; without one, the pool's own is used."""
+    decode_attn calls that may run at the same time need workspaces of their own.  Without a `workspace`
+    argument (workspace_bytes bytes) the pool keeps one for each stream, and a captured call gets one that no
+    other call uses, so that graphs may replay beside one another and beside eager calls."""
 
     def __init__(self, n_kv_heads, head_dim, page_size, n_pages, k_format="fp16", k_bits=16, k_group=0,
                  v_format="fp16", v_bits=16, v_group=0, buf: Optional[torch.Tensor] = None, device="cuda",
@@ -668,8 +669,8 @@ class PagedKVCache:
         _call(self._dev, stream, lambda st: lib.kvq_paged_init(byref(self.cfg), buf.data_ptr(), buf.numel(), st, byref(h)))
         self.handle = h
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
-        self._ws: Optional[torch.Tensor] = None
-        self._old_ws = []
+        self._ws = {}          # raw stream -> workspace
+        self._kept = []        # workspaces that captured graphs, or calls still in flight, may use
         self._need = {}
         self.launches = 0
 
@@ -725,11 +726,16 @@ class PagedKVCache:
         need = self._need.get(key)
         if need is None:
             need = self._need[key] = max(16, self.workspace_bytes(*key))
-        if self._ws is None or self._ws.numel() < need:
-            if self._ws is not None:
-                self._old_ws.append(self._ws)   # captured graphs may still use it
-            self._ws = _empty((need,), torch.uint8, self._dev, stream)
-        return self._ws
+        if torch.cuda.is_current_stream_capturing():
+            self._kept.append(_empty((need,), torch.uint8, self._dev, stream))
+            return self._kept[-1]
+        raw = _cur_stream(self._dev) if stream is None else _stream(stream)
+        ws = self._ws.get(raw)
+        if ws is None or ws.numel() < need:
+            if ws is not None:
+                self._kept.append(ws)
+            ws = self._ws[raw] = _empty((need,), torch.uint8, self._dev, stream)
+        return ws
 
     def decode_attn(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                     prefix_pages: Optional[torch.Tensor] = None, prefix_len: Optional[torch.Tensor] = None,

@@ -104,6 +104,7 @@ kvq::RopeView rope_view(const kvq_rope* rope) {
 kvq_status compute_layout(const kvq_paged_config* c, kvq_paged_layout* L) {
   if (!c || !L) return fail(KVQ_ERR_INVALID_ARG, "null paged config or layout");
   if (c->n_kv_heads < 1 || c->n_pages < 1) return fail(KVQ_ERR_INVALID_ARG, "n_kv_heads and n_pages must be >= 1");
+  if (c->n_kv_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "more than 65535 kv heads");
   if (c->head_dim != 64 && c->head_dim != 128)
     return fail(KVQ_ERR_UNSUPPORTED, "paged head_dim %d not supported (64, 128)", c->head_dim);
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)

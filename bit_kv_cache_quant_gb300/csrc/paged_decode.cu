@@ -213,9 +213,16 @@ cudaError_t launch_format(const PoolView& p, const OwnArgs& a, const PrefixArgs&
 size_t paged_workspace_bytes(const PoolView& p, int n_seqs, int Hq, int max_prefix_pages) {
   const int G = Hq / p.Hkv;
   const size_t states = (size_t)4 * p.sms + (size_t)n_seqs * p.Hkv;
+  // A smaller batch may be cut into more runs: the prefix's states are bounded
+  // by what fills the device once (256 rows a CTA) or by one run of every row.
   const Plan r = make_plan(p, n_seqs, G, max_prefix_pages);
-  return starts_bytes(n_seqs) + prefix_ml_bytes(p, r, n_seqs * G) + prefix_o_bytes(p, r, n_seqs * G) +
-         states * G * (p.D + kPartPad) * sizeof(float);
+  size_t prefix = 0;
+  if (r.shared) {
+    const size_t rows = (size_t)n_seqs * G > 256 ? (size_t)n_seqs * G : 256;
+    const size_t most = rows * p.Hkv > (size_t)256 * p.sms ? rows * p.Hkv : (size_t)256 * p.sms;
+    prefix = most * (p.D * sizeof(float) + sizeof(float2)) + 256;
+  }
+  return starts_bytes(n_seqs) + prefix + states * G * (p.D + kPartPad) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PoolView& p, const PagedDecodeArgs& d, cudaStream_t st) {

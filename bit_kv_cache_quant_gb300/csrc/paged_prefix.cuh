@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
       __syncwarp();
     }
     const float c = s_scale[qt * 128 + r] * a.qscale;
-    float m = neg_inf(), l = 0.0f;
+    float m = neg_inf(), l = 0.0f;   // the row's reference maximum (unscaled) and sum
 #pragma unroll 1
     for (int k = 0; k < mine_n; ++k) {
       const int j = NQ == 2 ? k : 2 * k + t;
@@ -321,10 +321,11 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
           t1 = fmaxf(fmaxf(t1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
         }
       };
+      // (the difference first: a scaled maximum's own rounding would count in whole powers at huge scores)
       auto weigh = [&](uint32_t(&x)[32], uint32_t* w, float2 base2) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 v = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, base2);
+          float2 v = mul2(add2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), base2), c2);
           v.x = fast_exp2(v.x);
           v.y = fast_exp2(v.y);
           sum = add2(sum, v);
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
         mask(xb, 3);
         highest(xb);
         weigh(xb, w1 + 16, base2);
-        stands = !__any_sync(0xffffffffu, fmaxf(t0, t1) * c > m + kSlack);
+        stands = !__any_sync(0xffffffffu, (fmaxf(t0, t1) - base) * c > kSlack);
         if (stands) {   // over scores this thread has read
           tmem_st32(ts + 64, w0);
           tmem_st32(ts + 96, w1);
@@ -372,11 +373,11 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
           mask(xa, i);
           highest(xa);
         }
-        const float top = fmaxf(t0, t1) * c;
+        const float top = fmaxf(t0, t1);
         const bool up = top > m;
         const float mn = up ? top : m;
         if (k > 0) {   // (the first tile's product overwrites the accumulators)
-          const float alpha = up ? fast_exp2(m - mn) : 1.0f;
+          const float alpha = up ? fast_exp2((m - mn) * c) : 1.0f;
           l *= alpha;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
     const bool mine = row < a.rows && !s_fail;
     const int slot = NQ == 2 ? blockIdx.x : 2 * blockIdx.x + t;
     const size_t at = ((size_t)kvh * a.nsplit * a.streams + slot) * a.rows + row;
-    if (mine) a.part_ml[at] = make_float2(m, l);
+    if (mine) a.part_ml[at] = make_float2(m * c, l);
     if (mine_n > 0) {
 #pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {

@@ -477,7 +477,7 @@ kvq_status kvq_rope_qk(const kvq_rows* q, const kvq_rows* k, int32_t n_tokens, i
    whole batch followed by each sequence's own pages. */
 
 typedef struct kvq_paged_config {
-  int32_t n_kv_heads;     /* >= 1 */
+  int32_t n_kv_heads;     /* 1 .. 65535 */
   int32_t head_dim;       /* 64 or 128 */
   int32_t page_size;      /* rows of a page: 16, 32, 64 or 128 */
   int32_t n_pages;        /* n_kv_heads * page_size * n_pages below 2^31 - 128 */

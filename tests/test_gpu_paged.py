@@ -454,3 +454,189 @@ def test_wait_that_runs_out_reports_and_recovers(kvq):
         kvq.kvq_test_stall_decode_tiles(False)
     c.clear_status()
     assert torch.equal(c.decode_attn(*args, **kw), want) and c.status() == 0
+
+
+# Prefixes long enough, for their batches, to be taken once for all sequences (on up to 152 SMs).
+SHARED = [
+    # (B, H, G, D, page, prefix)
+    (3, 8, 4, 64, 64, 11000),       # a dozen query rows per kv head, long runs
+    (65, 4, 1, 128, 16, 1025),      # one row tile, a tile of one row at the end
+    (33, 4, 4, 64, 32, 2100),       # rows just past one tile of 128
+    (100, 4, 8, 128, 128, 800),     # four CTAs of rows
+    (40, 8, 3, 128, 64, 897),
+]
+
+
+@pytest.mark.parametrize("fmt,kg,vg", [("fp16", 0, 0), ("aff8", 128, 32), ("aff4", 64, 64), ("aff4", 32, 128)])
+@pytest.mark.parametrize("shape", SHARED)
+def test_attention_prefix_taken_once(kvq, shape, fmt, kg, vg):
+    B, H, G, D, page, prefix = shape
+    lens = [(37 * b) % 70 for b in range(B)]
+    c, q, out = run_attention(kvq, fmt, H, G, D, page, lens, prefix, "bf16", kg or 64, vg or 64, seed=B)
+    assert c.launches == 3   # prefix, own rows, merge
+    table, pre, _ = tables(lens, prefix, page, seed=B)
+    kw = dict(prefix_pages=dev(pre), prefix_len=i32([prefix]))
+    assert torch.equal(c.decode_attn(q, dev(table), i32(lens), **kw), out)
+    run_attention(kvq, fmt, H, G, D, page, lens, prefix, "fp16", kg or 64, vg or 64, seed=B, qscale=4.0)
+
+
+def test_prefix_taken_once_follows_its_length(kvq):
+    # the plan goes by the tables' width, the work by the length on the device: from nothing to the whole table
+    B, H, G, D, page, most = 33, 4, 4, 64, 64, 2112
+    lens = [(11 * b) % 40 for b in range(B)]
+    table, pre, n = tables(lens, most, page, seed=61)
+    c = make_pool(kvq, "aff8", H, D, page, n, seed=62)
+    q = rand((B, H * G, D), torch.Generator().manual_seed(6), torch.bfloat16)
+    plen = i32([0])
+    for prefix in (0, 1, 127, 128, 129, 1000, 2111, 2112):
+        plen.fill_(prefix)
+        out = c.decode_attn(q, dev(table), i32(lens), prefix_pages=dev(pre), prefix_len=plen)
+        want, vm, sm = reference(q, values(c, "k"), values(c, "v"), table, lens, pre, prefix, page)
+        check_attention(out, want, vm, sm, f"prefix {prefix}")
+    assert c.status() == 0
+    plen.fill_(most + 1)
+    again = c.decode_attn(q, dev(table), i32(lens), prefix_pages=dev(pre), prefix_len=plen)
+    assert torch.equal(again, out) and c.status() == kvq.DEV_BAD_PAGE
+
+
+def test_prefix_taken_once_ignores_rows_past_the_length_and_bad_pages(kvq):
+    B, H, G, D, page, prefix = 33, 4, 4, 64, 64, 2100
+    lens = [(13 * b) % 30 for b in range(B)]
+    for fmt in ("fp16", "aff8", "aff4"):
+        table, pre, n = tables(lens, prefix, page, seed=71)
+        c = make_pool(kvq, fmt, H, D, page, n, seed=72)
+        q = rand((B, H * G, D), torch.Generator().manual_seed(7), torch.bfloat16)
+        args, kw = (q, dev(table), i32(lens)), dict(prefix_pages=dev(pre), prefix_len=i32([prefix]))
+        clean = c.decode_attn(*args, **kw)
+        live = np.zeros((n, page), dtype=bool)
+        for row, m in [(pre, prefix)] + list(zip(table, lens)):
+            ids, rows = opos.page_rows(row, m, page)
+            live[ids, rows] = True
+        for bad in (float("nan"), float("inf"), -65504.0):
+            for side in "kv":
+                c.plane(side + ("_codes" if fmt == "fp16" else "_meta")).transpose(1, 2)[dev(~live)] = bad
+            assert torch.equal(c.decode_attn(*args, **kw), clean), (fmt, bad)
+        # a page outside the pool is left out
+        kv, vv = values(c, "k"), values(c, "v")
+        hole = pre.copy()
+        hole[5] = n
+        out = c.decode_attn(*args, prefix_pages=dev(hole), prefix_len=i32([prefix]))
+        assert c.status() == kvq.DEV_BAD_PAGE
+        keep = np.delete(pre, 5)
+        want, vm, sm = reference(q, kv, vv, table, lens, keep, prefix - page, page)
+        check_attention(out, want, vm, sm, fmt)
+
+
+def test_prefix_taken_once_wait_that_runs_out(kvq):
+    B, H, G, D, page, prefix = 65, 4, 1, 64, 64, 1100
+    lens = [5] * B
+    for fmt in ("fp16", "aff4"):
+        table, pre, n = tables(lens, prefix, page, seed=81)
+        c = make_pool(kvq, fmt, H, D, page, n, seed=82)
+        q = rand((B, H * G, D), torch.Generator().manual_seed(8), torch.bfloat16)
+        args, kw = (q, dev(table), i32(lens)), dict(prefix_pages=dev(pre), prefix_len=i32([prefix]))
+        want = c.decode_attn(*args, **kw)
+        torch.cuda.synchronize()
+        kvq.kvq_test_stall_decode_tiles(True)
+        try:
+            c.decode_attn(*args, **kw)
+            assert c.status() == kvq.DEV_TIMEOUT
+        finally:
+            kvq.kvq_test_stall_decode_tiles(False)
+        c.clear_status()
+        assert torch.equal(c.decode_attn(*args, **kw), want) and c.status() == 0
+
+
+def test_workspace_covers_smaller_calls(kvq):
+    # bytes for "up to" n sequences and pages hold for fewer of either
+    c = make_pool(kvq, "fp16", 8, 64, 64, 1, fill=False)
+    for hq in (8, 32, 64):
+        for pages in (0, 3, 40, 600):
+            sizes = [c.workspace_bytes(n, hq, pages) for n in range(1, 400)]
+            assert sizes == sorted(sizes)
+            assert all(a <= b for a, b in zip(sizes[::37], [c.workspace_bytes(n, hq, pages + 100) for n in range(1, 400, 37)]))
+    small = c.decode_attn(torch.zeros((64, 32, 64), dtype=torch.bfloat16, device="cuda"), i32([[0]] * 64), i32([1] * 64),
+                          prefix_pages=i32([0] * 20), prefix_len=i32([1200]),
+                          workspace=torch.empty(c.workspace_bytes(300, 32, 40), dtype=torch.uint8, device="cuda"))
+    assert small.shape == (64, 32, 64) and c.status() == 0
+
+
+def test_extreme_values(kvq):
+    # queries from the ends of bf16's range, one key of -inf, values near fp16's largest
+    B, H, D, page = 33, 4, 64, 64
+    for prefix in (0, 2100):
+        lens = [40] * B
+        table, pre, n = tables(lens, prefix, page, seed=91)
+        c = make_pool(kvq, "fp16", H, D, page, n, seed=92)
+        c.plane("v_codes").mul_(1e4)
+        q = rand((B, H * 4, D), torch.Generator().manual_seed(9), torch.float32)
+        q[:, 0] *= 1e30
+        q[:, 1] *= 1e-30
+        q[:, 2] = 0
+        q = q.to(torch.bfloat16)
+        kw = dict(prefix_pages=dev(pre), prefix_len=i32([prefix])) if prefix else {}
+        out = c.decode_attn(q, dev(table), i32(lens), **kw)
+        want, vm, sm = reference(q, values(c, "k"), values(c, "v"), table, lens, pre, prefix, page)
+        # (head 0's softmax is one key's: its smax bound says nothing, its values are checked as they are)
+        check_attention(out[:, 1:], want[:, 1:], vm[:, 1:], sm[:, 1:], f"prefix {prefix}")
+        assert np.abs(host(out[:, 0]) - want[:, 0]).max() <= 2.0 ** -8 * np.abs(want[:, 0]).max() + 1e4 * 2.0 ** -10
+
+
+def test_groups_of_graphs_replay_together(kvq):
+    # two captured calls of one pool, replayed on two streams at once, keep out of each other's workspace
+    B, H, G, D, page, prefix = 33, 4, 4, 64, 64, 2100
+    lens = [(17 * b) % 200 for b in range(B)]
+    table, pre, n = tables(lens, prefix, page, seed=95)
+    c = make_pool(kvq, "aff4", H, D, page, n, seed=96)
+    t, l, pp, pl = dev(table), i32(lens), dev(pre), i32([prefix])
+    qs = [rand((B, H * G, D), torch.Generator().manual_seed(i), torch.bfloat16) for i in (1, 2)]
+    want = [c.decode_attn(q, t, l, prefix_pages=pp, prefix_len=pl) for q in qs]
+    outs, graphs = [torch.empty_like(q) for q in qs], []
+    for q, o in zip(qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.decode_attn(q, t, l, prefix_pages=pp, prefix_len=pl, out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_pages_beyond_4_gib(kvq):
+    # planes larger than 32 bits of bytes: the last pages of a 5 GiB plane hold what the first ones would
+    H, D, page, n = 8, 128, 128, 20480
+    c = make_pool(kvq, "fp16", H, D, page, n, fill=False)
+    small = make_pool(kvq, "fp16", H, D, page, 4, fill=False)
+    g = torch.Generator().manual_seed(97)
+    k, v = rand((300, H, D), g, torch.bfloat16), rand((300, H, D), g, torch.bfloat16)
+    q = rand((1, H * 4, D), g, torch.bfloat16)
+    outs = []
+    for pool, ids in ((c, [n - 1, 16500, n - 3]), (small, [3, 0, 1])):
+        pool.append(k, v, i32([ids]), i32([300]), cu_tokens=i32([0, 300]))
+        outs.append(pool.decode_attn(q, i32([ids]), i32([300])))
+        assert pool.status() == 0
+    assert torch.equal(outs[0], outs[1])
+    for a, b in zip([n - 1, 16500, n - 3], [3, 0, 1]):
+        assert torch.equal(c.plane("k_codes")[a], small.plane("k_codes")[b])
+
+
+def test_prefix_beyond_4_gib_taken_once(kvq):
+    H, D, page, n = 8, 128, 128, 20480
+    c = make_pool(kvq, "fp16", H, D, page, n, fill=False)
+    small = make_pool(kvq, "fp16", H, D, page, 12, fill=False)
+    g = torch.Generator().manual_seed(98)
+    k, v = rand((1100, H, D), g, torch.bfloat16), rand((1100, H, D), g, torch.bfloat16)
+    B = 33
+    q = rand((B, H * 4, D), g, torch.bfloat16)
+    outs = []
+    for pool, ids in ((c, list(range(n - 9, n))), (small, list(range(9)))):
+        pool.append(k, v, i32([ids]), i32([1100]), cu_tokens=i32([0, 1100]))
+        outs.append(pool.decode_attn(q, i32([[0]] * B), i32([0] * B), prefix_pages=i32(ids), prefix_len=i32([1100])))
+        assert pool.status() == 0 and pool.launches == 1 + 3
+    assert torch.equal(outs[0], outs[1])

@@ -187,7 +187,7 @@ def test_paged_layout(kvq):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(head_dim=96), 2), (dict(head_dim=32), 2), (dict(page_size=48), 2), (dict(page_size=256), 2),
-    (dict(n_pages=0), 1), (dict(n_kv_heads=0), 1), (dict(kb=2), 1), (dict(kg=16), 1), (dict(vg=48), 1),
+    (dict(n_pages=0), 1), (dict(n_kv_heads=0), 1), (dict(n_kv_heads=65536), 2), (dict(kb=2), 1), (dict(kg=16), 1), (dict(vg=48), 1),
     (dict(head_dim=64, kg=128), 1), (dict(kf="fp16", kb=4), 1), (dict(kf="q4_0", kb=4, kg=32), 2),
     (dict(kf="kivi_chan"), 2), (dict(kb=8), 2), (dict(kf="fp16", kb=16), 2),
     (dict(n_pages=2 ** 31 - 1, n_kv_heads=2 ** 31 - 1), 2), (dict(n_pages=2 ** 22), 2),
