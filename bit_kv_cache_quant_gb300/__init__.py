@@ -584,32 +584,36 @@ def _rows(name, x: torch.Tensor, out: Optional[torch.Tensor], weight: Optional[t
           head_dim: int, dtype) -> bytes:
     """kvq_rows of x [tokens, heads, head_dim], as packed bytes."""
     s = x.shape
-    if len(s) != 3 or s[0] != tokens or s[2] != head_dim or x.dtype is not dtype:
+    if len(s) != 3 or x.dtype is not dtype:
         raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}] {dtype}, got {tuple(s)} {x.dtype}")
+    n, heads, d = s
     i0, i1, i2 = x.stride()
+    if n != tokens or d != head_dim:
+        raise ValueError(f"{name} must be [{tokens}, heads, {head_dim}] {dtype}, got {tuple(s)} {x.dtype}")
     if i2 != 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
     o0 = o1 = optr = w = 0
     if out is not None:
-        o0, o1, o2 = out.stride()
-        if out.shape != s or out.dtype is not dtype or o2 != 1:
+        if out.shape != s or out.dtype is not dtype:
             raise ValueError(f"{name}_out must have {name}'s shape and dtype, its channels contiguous")
-        if (o0 == 0 and s[0] > 1) or (o1 == 0 and s[1] > 1):
+        o0, o1, o2 = out.stride()
+        if o2 != 1:
+            raise ValueError(f"{name}_out must have {name}'s shape and dtype, its channels contiguous")
+        if (not o0 and n > 1) or (not o1 and heads > 1):
             raise ValueError(f"{name}_out must not be an expanded tensor")
         optr = out.data_ptr()
     if weight is not None:
         if weight.shape != (head_dim,) or weight.dtype is not dtype or not weight.is_contiguous():
             raise ValueError(f"{name}_norm must be a contiguous [{head_dim}] tensor of {name}'s dtype")
         w = weight.data_ptr()
-    return _ROWS.pack(x.data_ptr(), optr, i0, i1, o0, o1, s[1], w)
+    return _ROWS.pack(x.data_ptr(), optr, i0, i1, o0, o1, heads, w)
 
 
 def _int32(name, t: Optional[torch.Tensor], n: int, cols: Optional[int] = None) -> int:
     """Pointer of a contiguous int32 tensor of n (or n x cols) entries; 0 for None."""
     if t is None:
         return 0
-    if (t.dtype is not torch.int32 or t.dim() != (1 if cols is None else 2) or t.size(0) != n
-            or (cols is not None and t.size(1) != cols) or not t.is_contiguous()):
+    if t.dtype is not torch.int32 or t.shape != ((n,) if cols is None else (n, cols)) or not t.is_contiguous():
         want = (n,) if cols is None else (n, cols)
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {want}, got {tuple(t.shape)} {t.dtype}")
     return t.data_ptr()
@@ -623,10 +627,12 @@ def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Opt
     given), then rotated by positions int32 [T] (rope None: norm only).  Strided q and k, and outputs that
     are the inputs themselves, are fine; either of q and k may be None."""
     x = q if q is not None else k
-    if x is None or x.dim() != 3 or x.dtype not in DTYPES:
+    s = None if x is None else x.shape
+    if s is None or len(s) != 3 or x.dtype not in DTYPES:
         raise ValueError("q and k must be [T, heads, D] fp32 / bf16 / fp16 tensors")
+    tokens, _, head_dim = s
+    dt = x.dtype
     dev = _device_of(x, k, positions, q_out, k_out, q_norm, k_norm, None if rope is None else rope.freqs)
-    tokens, head_dim, dt = x.size(0), x.size(2), x.dtype
     rq = rk = None
     if q is not None:
         if q_out is None:
@@ -682,9 +688,10 @@ class PagedKVCache:
 
     def _batch(self, page_table, seq_lens, prefix_pages, prefix_len) -> bytes:
         """kvq_paged_batch, as packed bytes."""
-        if page_table.dim() != 2 or seq_lens.dim() != 1 or page_table.size(0) != seq_lens.size(0):
+        s, n = page_table.shape, seq_lens.shape
+        if len(s) != 2 or len(n) != 1 or s[0] != n[0]:
             raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
-        B, cols = page_table.shape
+        B, cols = s
         npre = 0 if prefix_pages is None else prefix_pages.numel()
         if npre and prefix_len is None:
             raise ValueError("prefix_pages needs prefix_len")
@@ -701,18 +708,19 @@ class PagedKVCache:
         """Stores the step's new tokens k, v [T, Hkv, D] (k normed and rotated on the way) and returns q [T, Hq, D]
         normed and rotated.  seq_lens counts the new tokens; cu_tokens int32 [B + 1] gives each sequence's run of
         tokens (None: one each).  k_out, v_out: where to leave the values the stored rows stand for."""
-        if k.dim() != 3 or k.dtype not in DTYPES:
+        s = k.shape
+        if len(s) != 3 or k.dtype not in DTYPES:
             raise ValueError("k and v must be [T, Hkv, D] fp32 / bf16 / fp16 tensors")
         dev = _device_of(self.buf, k, v, page_table, seq_lens, cu_tokens, q, prefix_len, positions, q_out, k_out,
                          v_out, q_norm, k_norm, None if rope is None else rope.freqs)
-        tokens, dt, D = k.size(0), k.dtype, self.head_dim
+        tokens, dt, D = s[0], k.dtype, self.head_dim
         rq = None
         if q is not None:
             if q_out is None:
                 q_out = _empty(q.shape, dt, dev, stream)
             rq = _rows("q", q, q_out, q_norm, tokens, D, dt)
         _call(dev, stream, lib.kvq_paged_append, self.handle, self._batch(page_table, seq_lens, None, prefix_len), tokens,
-              _int32("cu_tokens", cu_tokens, page_table.size(0) + 1), rq, _rows("k", k, k_out, k_norm, tokens, D, dt),
+              _int32("cu_tokens", cu_tokens, page_table.shape[0] + 1), rq, _rows("k", k, k_out, k_norm, tokens, D, dt),
               _rows("v", v, v_out, None, tokens, D, dt), DTYPES[dt], None if rope is None else rope.arg,
               _int32("positions", positions, tokens), eps)
         self.launches += kvq_last_launch_count()
@@ -747,7 +755,7 @@ class PagedKVCache:
             raise ValueError(f"q must be a contiguous [B, Hq, {self.head_dim}] tensor, got {tuple(s)} {q.dtype}")
         dev = _device_of(self.buf, q, page_table, seq_lens, prefix_pages, prefix_len, out, workspace)
         batch = self._batch(page_table, seq_lens, prefix_pages, prefix_len)
-        if s[0] != page_table.size(0):
+        if s[0] != page_table.shape[0]:
             raise ValueError("q and page_table must have one row per sequence")
         if out is None:
             out = _empty(s, q.dtype, dev, stream)

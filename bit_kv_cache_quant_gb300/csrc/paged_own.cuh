@@ -21,7 +21,15 @@
 // A page holds whole 16-row blocks, so a block is on one page: a bad page id
 // takes its blocks out.
 //
-// Bound by HBM: 16 to 64 query rows per tile leave the tensor pipe idle.
+// Bound by instruction issue for packed rows: 33 ragged sequences up to 16K of 8
+// kv heads of 64, 8-bit pages of 16 rows, 288 MB in 90 us (47% of the measured
+// copy rate; issue 61% active, ALU pipe 49%); 120 sequences of five heads a kv
+// head, 4-bit, 71 MB in 53 us, where a second column tile for heads 5 to 8 took
+// 81.  For fp16 rows by the latency of short runs (67 MB in 21 us).  The same
+// products on tcgen05.mma (rows of the cache on the 128-row side, unpacked to
+// shared memory by their own warps) were right and slower, 186 and 178 us: every
+// role is long straight code run by one warp per scheduler, and instructions
+// did not arrive in time.
 #pragma once
 
 #include "decode_tc.cuh"
