@@ -207,7 +207,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int D, int F, int NQ>
-__global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_prefix_kernel(const __grid_constant__ PoolView p, const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1)
+    paged_prefix_kernel(const __grid_constant__ PoolView p, const __grid_constant__ PrefixArgs a) {
   using S = PrefixShape<D, F, NQ>;
   constexpr int KB = FmtBits<F>::v, ROW = D * KB / 8, RAW = ROW / 4, NST = S::kStages;
   constexpr bool AFF = F != F_FP16;
@@ -219,7 +220,9 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
   __shared__ __align__(8) uint64_t q_full, k_full[NST], k_empty[NST], v_full[NST], v_empty[NST], s_full[2], o_full[2],
       issued[2];
   __shared__ uint32_t s_tmem;
-  __shared__ uint32_t s_mask[4][4];   // live rows of tile j in ring slot j & 3
+  // Live rows of tile j, in ring slot j & 7.  A slot is written again when the scores of the fourth and
+  // third tile before are known to be done, hence the softmax of every tile up to the fifth before.
+  __shared__ uint32_t s_mask[8][4];
   __shared__ float s_scale[NQ * 128];
   __shared__ volatile int s_fail;
 
@@ -301,14 +304,14 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
       if (elect_one()) scores(j);
       __syncwarp();
     }
-    const float c = s_scale[qt * 128 + r] * a.qscale;
+    const float c = fmaxf(s_scale[qt * 128 + r] * a.qscale, 0x1p-149f);   // (never 0: -inf * c stays -inf)
     float m = neg_inf(), l = 0.0f;   // the row's reference maximum (unscaled) and sum
 #pragma unroll 1
     for (int k = 0; k < mine_n; ++k) {
       const int j = NQ == 2 ? k : 2 * k + t;
       wait(&s_full[t], k & 1);
       tc_fence_after();
-      volatile const uint32_t* live = s_mask[j & 3];
+      volatile const uint32_t* live = s_mask[j & 7];
       // Scores in quarters of 32 columns, the next one on its way while one is used.  Weights against the
       // row's reference maximum are kept back until all 128 scores have shown that it stands.
       uint32_t xa[32], xb[32];
@@ -366,7 +369,8 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
         mask(xb, 3);
         highest(xb);
         weigh(xb, w1 + 16, base2);
-        stands = !__any_sync(0xffffffffu, (fmaxf(t0, t1) - base) * c > kSlack);
+        // (a row that has had no live score yet has no reference to keep)
+        stands = !__any_sync(0xffffffffu, m == neg_inf() || (fmaxf(t0, t1) - base) * c > kSlack);
         if (stands) {   // over scores this thread has read
           tmem_st32(ts + 64, w0);
           tmem_st32(ts + 96, w1);
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(PrefixShape<D, F, NQ>::kThreads, 1) paged_pref
     for (int j = 0; j < n; ++j) {
       const int stg = j % NST;
       const uint32_t votes = __ballot_sync(0xffffffffu, ok);
-      if (keys && lane == 0) s_mask[j & 3][r >> 5] = votes;
+      if (keys && lane == 0) s_mask[j & 7][r >> 5] = votes;
       if (j >= NST) wait(&empty[stg], ((j / NST) & 1) ^ 1);
       uint8_t* tile = ring + stg * S::kTile;
       if (tma) {

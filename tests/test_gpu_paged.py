@@ -527,6 +527,33 @@ def test_prefix_taken_once_ignores_rows_past_the_length_and_bad_pages(kvq):
         check_attention(out, want, vm, sm, fmt)
 
 
+@pytest.mark.parametrize("fmt", ["fp16", "aff8", "aff4"])
+@pytest.mark.parametrize("B,G", [(33, 4), (33, 3)])   # two row tiles a CTA, and one
+def test_prefix_taken_once_starts_with_dead_tiles(kvq, fmt, B, G):
+    # whole tiles out of the pool in front of live ones, with scores too small to move a maximum: the first
+    # live tile sets the row's reference.  Also every page but the last one, and every page.
+    H, D, page, prefix = 4, 64, 64, 2100
+    lens = [0] * B
+    table, pre, n = tables(lens, prefix, page, seed=101)
+    c = make_pool(kvq, fmt, H, D, page, n, seed=102)
+    q = rand((B, H * G, D), torch.Generator().manual_seed(11), torch.bfloat16, 0.05)
+    kv, vv = values(c, "k"), values(c, "v")
+    for dead in (4, 16, len(pre) - 1, len(pre)):
+        hole = pre.copy()
+        hole[:dead] = -1
+        out = c.decode_attn(q, dev(table), i32(lens), prefix_pages=dev(hole), prefix_len=i32([prefix]))
+        assert c.status() == kvq.DEV_BAD_PAGE
+        want, vm, sm = reference(q, kv, vv, table, lens, pre[dead:], max(prefix - dead * page, 0), page)
+        check_attention(out, want, vm, sm, f"{fmt} {dead} dead pages")
+    # the same as every other page
+    hole = pre.copy()
+    hole[::2] = n
+    out = c.decode_attn(q, dev(table), i32(lens), prefix_pages=dev(hole), prefix_len=i32([prefix]))
+    keep = pre[1::2]
+    want, vm, sm = reference(q, kv, vv, table, lens, keep, len(keep) * page, page)
+    check_attention(out, want, vm, sm, f"{fmt} odd pages")
+
+
 def test_prefix_taken_once_wait_that_runs_out(kvq):
     B, H, G, D, page, prefix = 65, 4, 1, 64, 64, 1100
     lens = [5] * B
