@@ -515,6 +515,7 @@ def kvq_rope_table(cfg: kvq_rope_config):
 # checks below read each tensor's properties once, and arguments go as packed bytes in the C structs' layout.
 _cur_device = torch._C._cuda_getDevice
 _cur_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 _ROWS = struct.Struct("@PPqqqqiP")        # kvq_rows
 _BATCH = struct.Struct("@iiPPiPP")        # kvq_paged_batch
 
@@ -678,6 +679,7 @@ class PagedKVCache:
         self._ws = {}          # raw stream -> workspace
         self._kept = []        # workspaces that captured graphs, or calls still in flight, may use
         self._need = {}
+        self._plans = {}       # launches of a decode_attn
         self.launches = 0
 
     def __del__(self):
@@ -723,7 +725,7 @@ class PagedKVCache:
               _int32("cu_tokens", cu_tokens, page_table.shape[0] + 1), rq, _rows("k", k, k_out, k_norm, tokens, D, dt),
               _rows("v", v, v_out, None, tokens, D, dt), DTYPES[dt], None if rope is None else rope.arg,
               _int32("positions", positions, tokens), eps)
-        self.launches += kvq_last_launch_count()
+        self.launches += 1 if tokens else 0
         return q_out
 
     def workspace_bytes(self, n_seqs: int, n_q_heads: int, max_prefix_pages: int = 0) -> int:
@@ -734,7 +736,7 @@ class PagedKVCache:
         need = self._need.get(key)
         if need is None:
             need = self._need[key] = max(16, self.workspace_bytes(*key))
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing():
             self._kept.append(_empty((need,), torch.uint8, self._dev, stream))
             return self._kept[-1]
         raw = _cur_stream(self._dev) if stream is None else _stream(stream)
@@ -766,7 +768,11 @@ class PagedKVCache:
             ws = self._workspace(s[0], s[1], 0 if prefix_pages is None else prefix_pages.numel(), stream)
         _call(dev, stream, lib.kvq_paged_decode_attn, self.handle, batch, q.data_ptr(), out.data_ptr(), s[1],
               DTYPES[q.dtype], softmax_scale, ws.data_ptr(), ws.nbytes)
-        self.launches += kvq_last_launch_count()
+        key = (s[0], s[1], 0 if prefix_pages is None else prefix_pages.numel())
+        n = self._plans.get(key)
+        if n is None:      # the launch plan goes by these alone
+            n = self._plans[key] = kvq_last_launch_count()
+        self.launches += n
         return out
 
     def status(self) -> int:

@@ -21,7 +21,7 @@
 //
 // Bound by HBM for a prompt's rotation; by instruction issue with a norm (16K
 // tokens of 48 heads, 403 MB: 76 us, issue 71% active) or the coding of keys
-// and values (32K tokens into 8-bit pages, 874 MB: 180 us, issue 79%); by launch
+// and values (32K tokens into 8-bit pages, 874 MB: 175 us); by launch
 // latency for decode steps (2.3 us a launch for one token, 5.8 us for a step of
 // 64 into 4-bit pages).
 #include "paged.cuh"
@@ -479,9 +479,14 @@ __device__ __forceinline__ void copy16(uint4* dst, const uint4* src) {
 }
 
 // A warp takes one token and `rows_per_warp` groups of 32 / (D / 16) head rows;
-// groups never mix queries, keys and values.
+// groups never mix queries, keys and values.  Its rows are on their way before
+// the token's page and angles are looked up, and four CTAs to an SM cover the
+// issue slots (32K tokens into 8-bit pages 175 us, 9 prompts of 9K tokens into
+// fp16 pages of 16 36 us; with three CTAs 181 and 39); 32-bit rows need the
+// registers of three.
 template <int D, typename T, bool PAGED>
-__global__ void __launch_bounds__(32 * kRowWarps, PAGED || sizeof(T) == 4 ? 3 : 4) token_chunks_kernel(const __grid_constant__ TokenArgs a) {
+__global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 3 : 4)
+    token_chunks_kernel(const __grid_constant__ TokenArgs a) {
   constexpr int L = D / 16;     // lanes per row
   constexpr int R = 32 / L;     // rows per group
   constexpr int N = Eight<T>::N;
@@ -499,18 +504,46 @@ __global__ void __launch_bounds__(32 * kRowWarps, PAGED || sizeof(T) == 4 ? 3 : 
   const int g1 = min(g0 + a.rows_per_warp, total);
   if (g0 >= g1) return;
 
+  // Each lane copies its own channels ahead into its own slots of a ring, so
+  // the copies in flight cost no registers and wait for no other lane.
+  extern __shared__ __align__(16) uint4 ring[];
+  uint4* mine_ring = ring + warp * (kDepth<T> * 2 * N * 32) + lane;
+  auto row_of = [&](int g, int& kind) {   // head row of this lane in group g
+    kind = g < gq ? 0 : (g < gq + gk ? 1 : 2);
+    return (g - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * R + rg;
+  };
+  auto fetch = [&](int g) {
+    if (g < g1) {
+      int kind;
+      const int h = row_of(g, kind);
+      const RowsView& w = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+      // a group's spare lanes repeat the last row and store nothing
+      const T* src = static_cast<const T*>(w.in) + tok * w.in_tok + min(h, w.heads - 1) * w.in_head + 8 * l;
+      uint4* dst = mine_ring + (g - g0) % kDepth<T> * (2 * N * 32);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        copy16(dst + i * 32, reinterpret_cast<const uint4*>(src) + i);
+        copy16(dst + (N + i) * 32, reinterpret_cast<const uint4*>(src + D / 2) + i);
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth<T>; ++i) fetch(g0 + i);
+  auto leave = [] { asm volatile("cp.async.wait_all;\n" ::: "memory"); };   // nothing in flight at the end
+
   int pos = 0;
   long long page_row = -1;
   if constexpr (PAGED) {
     int b = tok, j = 0, n = 1;
     if (a.cu) {
       b = sequence_of(a.cu, a.batch.n_seqs, tok, lane);
-      if (b < 0) return;
+      if (b < 0) return leave();
       j = tok - a.cu[b];
       n = a.cu[b + 1] - a.cu[b];
     }
     const long long at = (long long)a.batch.lens[b] - n + j;
-    if (at < 0) return;
+    if (at < 0) return leave();
     pos = (int)at + (a.batch.prefix_len ? max(a.batch.prefix_len[0], 0) : 0);
     if (g1 > gq) {
       const long long col = at >> a.page_log2;
@@ -556,32 +589,6 @@ __global__ void __launch_bounds__(32 * kRowWarps, PAGED || sizeof(T) == 4 ? 3 : 
     }
   }
 
-  // Each lane copies its own channels ahead into its own slots of a ring, so
-  // the copies in flight cost no registers and wait for no other lane.
-  extern __shared__ __align__(16) uint4 ring[];
-  uint4* mine_ring = ring + warp * (kDepth<T> * 2 * N * 32) + lane;
-  auto row_of = [&](int g, int& kind) {   // head row of this lane in group g
-    kind = g < gq ? 0 : (g < gq + gk ? 1 : 2);
-    return (g - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * R + rg;
-  };
-  auto fetch = [&](int g) {
-    if (g < g1) {
-      int kind;
-      const int h = row_of(g, kind);
-      const RowsView& w = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-      // a group's spare lanes repeat the last row and store nothing
-      const T* src = static_cast<const T*>(w.in) + tok * w.in_tok + min(h, w.heads - 1) * w.in_head + 8 * l;
-      uint4* dst = mine_ring + (g - g0) % kDepth<T> * (2 * N * 32);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        copy16(dst + i * 32, reinterpret_cast<const uint4*>(src) + i);
-        copy16(dst + (N + i) * 32, reinterpret_cast<const uint4*>(src + D / 2) + i);
-      }
-    }
-    asm volatile("cp.async.commit_group;\n" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < kDepth<T>; ++i) fetch(g0 + i);
   int last_kind = -1;
   Eight<T> wl, wh;
   bool normed = false;
