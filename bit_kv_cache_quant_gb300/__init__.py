@@ -677,9 +677,8 @@ class PagedKVCache:
         self.handle = h
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
         self._ws = {}          # raw stream -> workspace
-        self._kept = []        # workspaces that captured graphs, or calls still in flight, may use
-        self._need = {}
-        self._plans = {}       # launches of a decode_attn
+        self._kept = []        # workspaces of captured calls
+        self._shapes = {}      # (n_seqs, n_q_heads, prefix pages) -> [workspace bytes, launches]
         self.launches = 0
 
     def __del__(self):
@@ -731,19 +730,14 @@ class PagedKVCache:
     def workspace_bytes(self, n_seqs: int, n_q_heads: int, max_prefix_pages: int = 0) -> int:
         return lib.kvq_paged_workspace_bytes(self.handle, n_seqs, n_q_heads, max_prefix_pages)
 
-    def _workspace(self, n_seqs, n_q_heads, npre, stream) -> torch.Tensor:
-        key = (n_seqs, n_q_heads, npre)
-        need = self._need.get(key)
-        if need is None:
-            need = self._need[key] = max(16, self.workspace_bytes(*key))
+    def _workspace(self, need, stream) -> torch.Tensor:
         if _capturing():
             self._kept.append(_empty((need,), torch.uint8, self._dev, stream))
             return self._kept[-1]
         raw = _cur_stream(self._dev) if stream is None else _stream(stream)
         ws = self._ws.get(raw)
         if ws is None or ws.numel() < need:
-            if ws is not None:
-                self._kept.append(ws)
+            # the smaller one goes back to the allocator, which orders it behind this stream's calls
             ws = self._ws[raw] = _empty((need,), torch.uint8, self._dev, stream)
         return ws
 
@@ -763,16 +757,18 @@ class PagedKVCache:
             out = _empty(s, q.dtype, dev, stream)
         elif out.shape != s or out.dtype is not q.dtype or not out.is_contiguous():
             raise ValueError("out must have q's shape and dtype")
-        ws = workspace
-        if ws is None:
-            ws = self._workspace(s[0], s[1], 0 if prefix_pages is None else prefix_pages.numel(), stream)
+        key = (s[0], s[1], 0 if prefix_pages is None else prefix_pages.numel())
+        shape = self._shapes.get(key)
+        if shape is None:      # workspace and launches go by these alone
+            if len(self._shapes) >= 4096:
+                self._shapes.clear()
+            shape = self._shapes[key] = [max(16, self.workspace_bytes(*key)), None]
+        ws = self._workspace(shape[0], stream) if workspace is None else workspace
         _call(dev, stream, lib.kvq_paged_decode_attn, self.handle, batch, q.data_ptr(), out.data_ptr(), s[1],
               DTYPES[q.dtype], softmax_scale, ws.data_ptr(), ws.nbytes)
-        key = (s[0], s[1], 0 if prefix_pages is None else prefix_pages.numel())
-        n = self._plans.get(key)
-        if n is None:      # the launch plan goes by these alone
-            n = self._plans[key] = kvq_last_launch_count()
-        self.launches += n
+        if shape[1] is None:
+            shape[1] = kvq_last_launch_count()
+        self.launches += shape[1]
         return out
 
     def status(self) -> int:

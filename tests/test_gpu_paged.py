@@ -667,3 +667,16 @@ def test_prefix_beyond_4_gib_taken_once(kvq):
         outs.append(pool.decode_attn(q, i32([[0]] * B), i32([0] * B), prefix_pages=i32(ids), prefix_len=i32([1100])))
         assert pool.status() == 0 and pool.launches == 1 + 3
     assert torch.equal(outs[0], outs[1])
+
+
+def test_a_growing_batch_keeps_one_workspace(kvq):
+    # a pool's own workspace grows with the batch; the smaller ones are given back
+    c = make_pool(kvq, "fp16", 8, 64, 64, 1, fill=False)
+    pages, plen = i32([0] * 40), i32([2500])
+    q, out = torch.zeros((2, 400, 32, 64), dtype=torch.bfloat16, device="cuda")
+    tab, lens = i32([[0]] * 400), i32([1] * 400)
+    before = torch.cuda.memory_allocated()
+    for n in range(2, 401, 2):
+        c.decode_attn(q[:n], tab[:n], lens[:n], prefix_pages=pages, prefix_len=plen, out=out[:n])
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - before <= c.workspace_bytes(400, 32, 40) + (2 << 20)
