@@ -21,7 +21,7 @@
 //
 // Bound by HBM for a prompt's rotation; by instruction issue with a norm (16K
 // tokens of 48 heads, 403 MB: 76 us, issue 71% active) or the coding of keys
-// and values (32K tokens into 8-bit pages, 874 MB: 175 us); by launch
+// and values (32K tokens into 8-bit pages, 874 MB: 175 us, issue 82%); by launch
 // latency for decode steps (2.3 us a launch for one token, 5.8 us for a step of
 // 64 into 4-bit pages).
 #include "paged.cuh"
