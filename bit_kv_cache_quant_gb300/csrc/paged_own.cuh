@@ -121,10 +121,33 @@ __device__ __forceinline__ void signed_bytes(uint32_t x, __half2& lo, __half2& h
   hi = __hsub2(hi, off);
 }
 
+// A code u in the low bits of an fp16 word is the subnormal number u * 2^-24, exact
+// in a product; u sixteen times as large sits four bits up.
+constexpr float kSubnormal = 0x1p-24f;
+__device__ __forceinline__ void low_bytes(uint32_t x, __half2& lo, __half2& hi) {   // u - 128 as signed bytes
+  x ^= 0x80808080u;
+  lo = u2h(__byte_perm(x, 0u, 0x4140u));
+  hi = u2h(__byte_perm(x, 0u, 0x4342u));
+}
+__device__ __forceinline__ void low_nibbles(uint32_t w, __half2 (&h)[4]) {   // as nibbles_to_h2, 16 u in h[1] and h[3]
+  const uint32_t w8 = w >> 8;
+  h[0] = u2h(w & 0x000F000Fu);
+  h[1] = u2h(w & 0x00F000F0u);
+  h[2] = u2h(w8 & 0x000F000Fu);
+  h[3] = u2h(w8 & 0x00F000F0u);
+}
+
+// How codes of values enter a product.
+enum ValueCodes : int {
+  kDecoded = 0,   // times scale plus zero, rounded to fp16
+  kSigned = 1,    // u - 8 or u - 128: half the size, where weights have no residual
+  kRaw = 2,       // u * 2^-24 (4-bit: 16 u * 2^-24 on rows 8 to 15 of an m-tile)
+};
+
 // O^T += V^T . P^T for one 16-row block and every column tile, as pvt_mma
 // (decode_tc.cuh): words A, B, C, E of the thread's rows 2t, 2t + 1, 2t + 8, 2t
-// + 9 feed m-tiles mo on.  Codes enter as u - kOff, with DEQ times scale plus zero.
-template <int KB, int HT, int NW, int MT, bool DEQ>
+// + 9 feed m-tiles mo on.
+template <int KB, int HT, int NW, int MT, int VC>
 __device__ __forceinline__ void value_products(float (&oacc)[HT][MT][4], const uint32_t (&pb)[HT][2], int mo,
                                                const uint32_t (&A)[NW], const uint32_t (&B)[NW],
                                                const uint32_t (&C)[NW], const uint32_t (&E)[NW], __half2 sAB,
@@ -145,9 +168,13 @@ __device__ __forceinline__ void value_products(float (&oacc)[HT][MT][4], const u
         if constexpr (KB == 4) {
           const uint32_t sel = half ? 0x7632u : 0x5410u;
           __half2 h0[4], h1[4];   // h0[i]: channel 8 wi + 4 half + i of rows A, B
-          nibbles_to_h2<DEQ ? 0 : 8>(__byte_perm(A[wi], B[wi], sel), h0);
-          nibbles_to_h2<DEQ ? 0 : 8>(__byte_perm(C[wi], E[wi], sel), h1);
-          if constexpr (DEQ) {
+          auto unpack = [](uint32_t w, __half2(&h)[4]) {
+            if constexpr (VC == kRaw) low_nibbles(w, h);
+            else nibbles_to_h2<VC == kDecoded ? 0 : 8>(w, h);
+          };
+          unpack(__byte_perm(A[wi], B[wi], sel), h0);
+          unpack(__byte_perm(C[wi], E[wi], sel), h1);
+          if constexpr (VC == kDecoded) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               h0[i] = __hfma2(h0[i], sAB, zAB);
@@ -162,7 +189,10 @@ __device__ __forceinline__ void value_products(float (&oacc)[HT][MT][4], const u
         } else {
           const uint32_t sel = half ? 0x7362u : 0x5140u;   // channels 4 wi + 2 half + 0 / 1
           __half2 l0, h0, l1, h1;
-          if constexpr (DEQ) {
+          if constexpr (VC == kRaw) {
+            low_bytes(__byte_perm(A[wi], B[wi], sel), l0, h0);
+            low_bytes(__byte_perm(C[wi], E[wi], sel), l1, h1);
+          } else if constexpr (VC == kDecoded) {
             bytes_to_h2(__byte_perm(A[wi], B[wi], sel) ^ 0x80808080u, l0, h0);
             bytes_to_h2(__byte_perm(C[wi], E[wi], sel) ^ 0x80808080u, l1, h1);
             l0 = __hfma2(l0, sAB, zAB); h0 = __hfma2(h0, sAB, zAB);
@@ -188,7 +218,10 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
   constexpr bool AFF = S::kAff;
   constexpr int NACC = AFF ? NB : 1;
   constexpr int HT = S::HT, NS = M == kPairs ? 1 : 2;   // column tiles; heads whose state a thread holds
-  constexpr int kOff = KB == 4 ? 8 : (KB == 8 ? 128 : 0);   // codes enter as u - kOff, zeros as z + kOff * s
+  // Codes of keys enter raw, those of values under one scale and zero a row raw or less kOff (zeros as z +
+  // kOff * s).  Queries enter below 2^kUp, so that the smaller channels next to a subnormal code stay exact.
+  constexpr int VFOLD = M == kSingles ? kSigned : kRaw, kOff = VFOLD == kRaw ? 0 : (KB == 4 ? 8 : 128);
+  constexpr int kUp = AFF ? 13 : 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float(*sm_acc)[S::kHeads][D + 8] = reinterpret_cast<float(*)[S::kHeads][D + 8]>(smem + NST * S::kStage);
@@ -364,6 +397,8 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
                        blk + tau<ROW>(2 * t + 9)};
     const int vgi = AFF ? (g * VCH) / p.v.group : 0;
     const bool vfold = AFF && vng == 1;
+    // what brings the two halves of an m-tile back to size
+    const float up0 = vfold && VFOLD == kRaw ? 1.0f / kSubnormal : 1.0f, up1 = KB == 4 && up0 != 1.0f ? up0 / 16 : up0;
     // the states of the thread's heads: 4 s + t in pairs, 2 t + s in singles
     float m_run[NS], l_part[NS], zacc[NS], qmul[NS];
     float oacc[HT][MT][4];
@@ -401,7 +436,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
           const bool live = hq < a.G;
           float xq[KS][4];
           load_query_channels<D, KB>(vmt + S::kMeta, (size_t)(live ? hq : 0) * D, a.io_dtype, t, live, xq);
-          // a power of two brings the head's largest magnitude under one (bf16's range in fp16)
+          // a power of two brings the head's largest magnitude under 2^kUp (bf16's range in fp16)
           float big = 0.0f;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks)
@@ -411,8 +446,8 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
           int ex = 0;
           if (big > 0.0f && big < __int_as_float(0x7f800000)) frexpf(big, &ex);
-          ex = max(min(ex, 126), -126);
-          const float down = __int_as_float((127 - ex) << 23);
+          ex = max(min(ex, 126), kUp - 126);
+          const float down = __int_as_float((127 + kUp - ex) << 23);
           const float mul = __int_as_float((127 + ex) << 23) * a.qscale;
           float qb[NB];
 #pragma unroll
@@ -425,6 +460,9 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
             if constexpr (AFF) qb[ks >> 1] += (x[0] + x[1]) + (x[2] + x[3]);
             // (exact: an odd column of a pair, the queries' residual, is zero)
             const bool zero = M != kSingles && (g & 1);
+            if (KB == 4 && (ks & 1))   // these channels' codes are 16 u
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] *= 0.0625f;
             qf[ht][ks][0] = zero ? 0u : h2u(__floats2half2_rn(x[0], x[1]));
             qf[ht][ks][1] = zero ? 0u : h2u(__floats2half2_rn(x[2], x[3]));
           }
@@ -432,7 +470,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
               qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], 1);
-              qb[i] += __shfl_xor_sync(0xffffffffu, qb[i], 2);
+              qb[i] = (qb[i] + __shfl_xor_sync(0xffffffffu, qb[i], 2)) * kSubnormal;
             }
           }
           // for the thread's own heads: the sums of q over each key group, and what brings scores back to scale
@@ -469,8 +507,8 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
 #pragma unroll
           for (int pb = 0; pb < NB; ++pb) {
             __half2 h0[4], h1[4];
-            nibbles_to_h2<kOff>(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * pb + 4 * t)), h0);
-            nibbles_to_h2<kOff>(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * pb + 4 * t)), h1);
+            low_nibbles(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * pb + 4 * t)), h0);
+            low_nibbles(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * pb + 4 * t)), h1);
             const uint32_t ka0[4] = {h2u(h0[0]), h2u(h1[0]), h2u(h0[2]), h2u(h1[2])};
             const uint32_t ka1[4] = {h2u(h0[1]), h2u(h1[1]), h2u(h0[3]), h2u(h1[3])};
 #pragma unroll
@@ -483,8 +521,8 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             __half2 l0, h0, l1, h1;
-            signed_bytes(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * ks + 4 * t)), l0, h0);
-            signed_bytes(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * ks + 4 * t)), l1, h1);
+            low_bytes(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[0], 16 * ks + 4 * t)), l0, h0);
+            low_bytes(*reinterpret_cast<const uint32_t*>(kst + swz_off<ROW>(rk[1], 16 * ks + 4 * t)), l1, h1);
             const uint32_t ka[4] = {h2u(l0), h2u(l1), h2u(h0), h2u(h1)};
 #pragma unroll
             for (int ht = 0; ht < HT; ++ht) mma_f16(acc[ht][ks >> 1], ka, qf[ht][ks][0], qf[ht][ks][1]);
@@ -499,7 +537,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
             for (int ht = 0; ht < HT; ++ht) mma_f16(acc[ht][0], ka, qf[ht][ks][0], qf[ht][ks][1]);
           }
         }
-        // s * sum(q u') + z' * sum(q) per scale group of 32, 64 or 128 channels
+        // s * sum(q u) + z * sum(q) per scale group of 32, 64 or 128 channels
         bool vk[2];
         float sc[NS][2];
 #pragma unroll
@@ -519,10 +557,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
               ws[0] = *reinterpret_cast<const uint32_t*>(mrow);
             }
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              sz[j] = __half22float2(u2h(ws[j]));
-              sz[j].y = fmaf((float)kOff, sz[j].x, sz[j].y);
-            }
+            for (int j = 0; j < NB; ++j) sz[j] = __half22float2(u2h(ws[j]));
           }
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
@@ -548,6 +583,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
             } else {
               v = got(0);
             }
+            if constexpr (AFF) v *= 1.0f / (kSubnormal * (1 << kUp));   // (qmul alone may be near fp32's largest)
             sc[s][e] = vk[e] ? v * qmul[s] : neg_inf();
           }
         }
@@ -605,7 +641,7 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
             for (int e = 0; e < 2; ++e) {
               float2 sz = __half22float2(u2h(vm[rk[e]]));
               if (!vk[e]) sz = make_float2(0.0f, 0.0f);
-              sz.y = fmaf((float)kOff, sz.x, sz.y);
+              if constexpr (kOff != 0) sz.y = fmaf((float)kOff, sz.x, sz.y);
 #pragma unroll
               for (int s = 0; s < NS; ++s) {
                 zacc[s] = fmaf(pr[s][e], sz.y, zacc[s]);
@@ -658,8 +694,8 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
             }
           }
           const int mo = w0 * (MT / NWT);
-          if (AFF && !vfold) value_products<KB, HT, NW, MT, true>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
-          else value_products<KB, HT, NW, MT, false>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
+          if (AFF && !vfold) value_products<KB, HT, NW, MT, kDecoded>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
+          else value_products<KB, HT, NW, MT, VFOLD>(oacc, pb, mo, A, B, C, E, sAB, zAB, sCD, zCD);
         }
       };
       const bool take = blk < nv && !s_fail && !((s_bad[stg] >> (warp & 3)) & 1);   // warp-uniform
@@ -685,8 +721,8 @@ __global__ void __launch_bounds__(OwnShape<D, F, M>::kThreads, OwnShape<D, F, M>
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const float(&o)[4] = oacc[M == kTwoTiles ? s : kNone][mt];
-            sm_acc[warp][head][(2 * mt) * 8 + g] = (M == kSingles ? o[s] : o[0] + o[1]) + zacc[s];
-            sm_acc[warp][head][(2 * mt + 1) * 8 + g] = (M == kSingles ? o[2 + s] : o[2] + o[3]) + zacc[s];
+            sm_acc[warp][head][(2 * mt) * 8 + g] = fmaf(M == kSingles ? o[s] : o[0] + o[1], up0, zacc[s]);
+            sm_acc[warp][head][(2 * mt + 1) * 8 + g] = fmaf(M == kSingles ? o[2 + s] : o[2] + o[3], up1, zacc[s]);
           }
           if (g == 0) {
             sm_m[warp][head] = m_run[s];
