@@ -17,13 +17,16 @@
 // the contiguous cache's decode (decode_tc.cuh): transposed products on
 // mma.sync m16n8k16 with 16 rows of keys or channels of values on the wide
 // side and the heads on the narrow one (Columns), keys
-// as exact integer codes with one fp32 accumulator per 32 channels.
+// as exact codes with one fp32 accumulator per 32 channels.
 // A page holds whole 16-row blocks, so a block is on one page: a bad page id
 // takes its blocks out.
 //
 // Bound by instruction issue for packed rows: 33 ragged sequences up to 16K of 8
-// kv heads of 64, 8-bit pages of 16 rows, 288 MB in 90 us (47% of the measured
-// copy rate; issue 61% active, ALU pipe 49%); 120 sequences of five heads a kv
+// kv heads of 64, 8-bit pages of 16 rows, 288 MB in 88 us (48% of the measured
+// copy rate; issue 57% active, ALU pipe 50%), of which the copies of 1 KB and 64
+// bytes without any product take four fifths (metadata in 16-byte pieces by the
+// copying lanes: the same here, 2 us more on pages of 64); codes converted to
+// fp16 integers took 90.  120 sequences of five heads a kv
 // head, 4-bit, 71 MB in 53 us, where a second column tile for heads 5 to 8 took
 // 81.  For fp16 rows by the latency of short runs (67 MB in 21 us).  The same
 // products on tcgen05.mma (rows of the cache on the 128-row side, unpacked to

@@ -680,3 +680,25 @@ def test_a_growing_batch_keeps_one_workspace(kvq):
         c.decode_attn(q[:n], tab[:n], lens[:n], prefix_pages=pages, prefix_len=plen, out=out[:n])
     torch.cuda.synchronize()
     assert torch.cuda.memory_allocated() - before <= c.workspace_bytes(400, 32, 40) + (2 << 20)
+
+
+@pytest.mark.parametrize("fmt,G,dtype", [("aff8", 4, torch.bfloat16), ("aff4", 4, torch.bfloat16),
+                                         ("aff4", 8, torch.bfloat16), ("aff8", 8, torch.float16)])
+def test_extreme_queries_next_to_stored_codes(kvq, fmt, G, dtype):
+    # the power of two that brings a query to its codes' size, at both ends of it
+    B, H, D, page = 3, 2, 64, 32
+    lens = [1, 40, 70]
+    table, pre, n = tables(lens, 0, page, seed=101)
+    c = make_pool(kvq, fmt, H, D, page, n, kgroup=64, vgroup=64, seed=102)
+    q = rand((B, H * G, D), torch.Generator().manual_seed(10), torch.float32)
+    bf = dtype is torch.bfloat16
+    q[:, 0] *= 1e30 if bf else 1e4
+    q[:, 1] *= 1e-37 if bf else 1e-6
+    q[:, 2] = 0
+    q = q.to(dtype)
+    out = c.decode_attn(q, dev(table), i32(lens))
+    want, vm, sm = reference(q, values(c, "k"), values(c, "v"), table, lens, pre, 0, page)
+    # (head 0's softmax is one key's: its smax bound says nothing, a rounding of weight 1 and of the output remain)
+    check_attention(out[:, 1:], want[:, 1:], vm[:, 1:], sm[:, 1:], fmt)
+    err = np.abs(host(out[:, 0]) - want[:, 0])
+    assert (err <= torch.finfo(dtype).eps * np.abs(want[:, 0]) + 2.0 ** -10 * np.abs(want[:, 0]).max()).all()
